@@ -125,6 +125,44 @@ PKV_API pkv_status pkv_kv_append(const pkv_cache_desc* desc, void* k_cache,
                          const void* k, const void* v, int32_t num_tokens,
                          pkv_dtype kv_dtype, pkv_stream_t stream);
 
+/* Flags of pkv_kv_append_rope. */
+#define PKV_ROPE_INTERLEAVED 1
+
+/* pkv_kv_append with the rotary position embedding applied on the way: the
+ * new tokens' q and k are rotated by their positions, q is written to q_out
+ * (for the attention call) and k and v to their slots, in one pass.
+ *   positions    int64 [num_tokens]: the row of cos_sin a token is turned by.
+ *   cos_sin      fp32 [max_position][rot_dim], 16-byte aligned: for each
+ *                position rot_dim / 2 cosines, then rot_dim / 2 sines.  Any
+ *                scaling of the angles or lengths is in the table.
+ *   rot_dim      elements of a head that turn, a multiple of 16, at most
+ *                head_dim; those after them are copied.  Pair i of a head is
+ *                elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ *                PKV_ROPE_INTERLEAVED, and becomes
+ *                (x0 cos_i - x1 sin_i, x1 cos_i + x0 sin_i), computed in fp32
+ *                and rounded once: to the type of q, to the 16-bit cache's
+ *                type, or by the E4M3 encoding of pkv_kv_append (whose
+ *                per-token scales are those of the rotated row).
+ *   q, k, v      token t's heads, each head_dim elements and one after the
+ *                other, start at element t * q_stride (k_stride, v_stride):
+ *                the parts of one fused projection can be passed as they lie.
+ *                Strides are multiples of 8 and at least a token's row; dtype
+ *                is F16 or BF16 for all three (for 16-bit caches the cache's).
+ *   q_out        [num_tokens][num_q_heads][head_dim]; may be q itself when
+ *                q_stride is exactly one row, otherwise must not overlap q, k
+ *                or v.
+ * A negative slot skips the token's k and v (its q is still rotated); a slot
+ * past the pool is a device-detected PKV_ERR_BOUNDS and skips them too.  A
+ * position outside [0, max_position) is PKV_ERR_BOUNDS and nothing of that
+ * token is written.  Slots written by two tokens of one call race; the caller
+ * avoids it. */
+PKV_API pkv_status pkv_kv_append_rope(
+    const pkv_cache_desc* desc, void* k_cache, void* v_cache, const int64_t* slot_mapping,
+    const int64_t* positions, const float* cos_sin, int32_t max_position, int32_t rot_dim,
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, void* q_out, int32_t num_tokens, pkv_dtype dtype, int32_t flags,
+    pkv_stream_t stream);
+
 /* Bytes of device workspace pkv_paged_decode_attention / pkv_decode_step
  * need for these sizes on the current device (it depends on the SM count).
  * Returns 0 on invalid arguments or without a device.  The workspace holds
@@ -253,6 +291,68 @@ PKV_API pkv_status pkv_paged_decode_attention_window(
     float scale, void* out, pkv_dtype q_dtype, pkv_dtype out_dtype,
     void* workspace, size_t workspace_bytes, pkv_stream_t stream);
 
+/* pkv_paged_decode_attention with the scores changed before the softmax, for
+ * models trained with capped scores or with a distance bias.  The score of
+ * query position t (context_lens[b] - 1) and key position u is
+ *   s = scale q.k;  s = softcap tanh(s / softcap) if softcap > 0;
+ *   s = s + alibi_slopes[hq] (u - t) if alibi_slopes is given.
+ *   window, sinks as for pkv_paged_decode_attention_window (0: no window).
+ *   softcap       0 (no cap), or between 2^-10 and 2^20.
+ *   alibi_slopes  device fp32 [num_q_heads], or NULL.
+ * With neither, the call is pkv_paged_decode_attention (or _window) itself.
+ * Other arguments, workspace and guarantees as for
+ * pkv_paged_decode_attention. */
+PKV_API pkv_status pkv_paged_decode_attention_biased(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int32_t batch, int32_t window, int32_t sinks,
+    float softcap, const float* alibi_slopes, int32_t max_blocks_per_seq,
+    int32_t max_context_len_hint, float scale, void* out, pkv_dtype q_dtype,
+    pkv_dtype out_dtype, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream);
+
+/* Bytes of device workspace pkv_paged_decode_attention_shared_prefix needs on
+ * the current device; rules as for pkv_decode_workspace_bytes (zero-filled
+ * once, serves every batch of at most B and any number of prefix blocks).
+ * Returns 0 on invalid arguments or without a device. */
+PKV_API size_t pkv_shared_prefix_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                         int32_t num_prefix_blocks,
+                                         int32_t max_blocks_per_seq,
+                                         int32_t max_context_len_hint);
+
+/* pkv_paged_decode_attention for a batch whose sequences all begin with the
+ * same blocks (a system prompt, a document, samples of one prompt; [KVFA]
+ * PagedAttention section, [AP] "Paged attention: stop reserving empty
+ * tables": sequences point at the same physical blocks for a shared
+ * beginning).  The prefix is read once for the whole batch: a dense product
+ * of all query rows of a KV head with its blocks on the tensor cores
+ * (tcgen05), merged with each sequence's attention over its own blocks.
+ *   prefix_blocks      device int32 [num_prefix_blocks]: the blocks of
+ *                      positions 0 .. 16 num_prefix_blocks - 1 of every
+ *                      sequence.
+ *   num_prefix_blocks  0 .. max_blocks_per_seq (0: no prefix).
+ *   block_tables       the sequences' whole tables; their first
+ *                      num_prefix_blocks entries are not read and may be
+ *                      anything.
+ *   context_lens       whole lengths, the prefix included.  A sequence
+ *                      shorter than the prefix sees the positions before its
+ *                      length.
+ *   scale              > 0.
+ * 16-bit caches (E4M3 returns PKV_ERR_UNSUPPORTED).  Short prefixes and small
+ * batches, where the separate passes cost more than they save, take one
+ * kernel that reads the prefix for each sequence.  Results are bitwise
+ * repeatable.  Values of the prefix behind a sequence's length, but inside
+ * another's, meet a weight of zero: they must be finite.  Other arguments and
+ * guarantees as for pkv_paged_decode_attention. */
+PKV_API pkv_status pkv_paged_decode_attention_shared_prefix(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* prefix_blocks,
+    int32_t num_prefix_blocks, const int32_t* block_tables,
+    const int32_t* context_lens, int32_t batch, int32_t max_blocks_per_seq,
+    int32_t max_context_len_hint, float scale, void* out, pkv_dtype q_dtype,
+    pkv_dtype out_dtype, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream);
+
 /* One whole decode step: pkv_kv_append of one new token per sequence
  * (slot_mapping, k, v have `batch` rows) followed by
  * pkv_paged_decode_attention, validated together before anything is
@@ -302,6 +402,17 @@ PKV_API pkv_status pkv_paged_prefill_attention(
     int32_t total_q, int32_t max_q_len, int32_t max_blocks_per_seq,
     float scale, void* out, pkv_dtype q_dtype, pkv_dtype out_dtype,
     pkv_stream_t stream);
+
+/* pkv_paged_prefill_attention with the scores changed before the softmax as
+ * by pkv_paged_decode_attention_biased (t the query row's position).  Other
+ * arguments and guarantees as for pkv_paged_prefill_attention. */
+PKV_API pkv_status pkv_paged_prefill_attention_biased(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* q_start, int32_t batch,
+    int32_t total_q, int32_t max_q_len, int32_t max_blocks_per_seq,
+    float scale, float softcap, const float* alibi_slopes, void* out,
+    pkv_dtype q_dtype, pkv_dtype out_dtype, pkv_stream_t stream);
 
 /* One decode step in ONE kernel: pkv_decode_step with each sequence's new
  * token placed at its position context_lens[b] - 1, i.e. in block

@@ -5,6 +5,8 @@ kernels behind the C ABI declared in ``include/pkv.h``; torch supplies device
 memory and streams.  The functions carry the C names:
 
     pkv_kv_append                 write new K/V rows into their cache slots
+    pkv_kv_append_rope            the same with q and k rotated by their
+                                  positions (rotary embedding) on the way
     pkv_decode_workspace_bytes    workspace size for a decode call
     pkv_decode_workspace_bytes_multi  the same for q_len query tokens per
                                   sequence (multi-query and windowed calls)
@@ -12,8 +14,15 @@ memory and streams.  The functions carry the C names:
     pkv_paged_decode_attention_multi  q_len new tokens per sequence, causal
     pkv_paged_decode_attention_window  the same under a sliding window with
                                   attention sinks
+    pkv_paged_decode_attention_biased  decode with scores capped by a tanh, a
+                                  distance bias, or both
+    pkv_paged_decode_attention_shared_prefix  decode for a batch whose
+                                  sequences begin with the same blocks, read
+                                  once for all of them
+    pkv_shared_prefix_workspace_bytes  workspace size for that call
     pkv_paged_prefill_attention   a chunk of new tokens per sequence, causal,
                                   on the tensor cores (tcgen05)
+    pkv_paged_prefill_attention_biased  the same with capped or biased scores
     pkv_decode_step               both, validated together, the attention
                                   kernel overlapping the append's tail
     pkv_decode_step_fused         both in one kernel (new token at its
@@ -46,7 +55,10 @@ __all__ = [
     "pkv_paged_decode_attention_noalloc", "PKV_NOALLOC_SCRATCH_BYTES", "pkv_copy_blocks",
     "pkv_decode_workspace_bytes_multi",
     "pkv_paged_decode_attention_multi", "pkv_paged_decode_attention_window",
-    "pkv_decode_step_fused", "pkv_paged_prefill_attention",
+    "pkv_decode_step_fused", "pkv_paged_prefill_attention", "pkv_kv_append_rope",
+    "pkv_paged_decode_attention_biased", "pkv_paged_prefill_attention_biased",
+    "pkv_paged_decode_attention_shared_prefix", "pkv_shared_prefix_workspace_bytes",
+    "PKV_ROPE_INTERLEAVED",
     "PKV_OK", "PKV_ERR_INVALID_ARG", "PKV_ERR_UNSUPPORTED", "PKV_ERR_WORKSPACE",
     "PKV_ERR_CUDA", "PKV_ERR_BOUNDS", "PKV_ERR_TIMEOUT",
     "PKV_F16", "PKV_BF16", "PKV_FP8_E4M3", "PKV_F32", "PKV_FP8_E4M3_TOKEN", "PKV_STEP_OVERLAP",
@@ -57,13 +69,16 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE = 0, 1, 2, 3
 PKV_ERR_CUDA, PKV_ERR_BOUNDS, PKV_ERR_TIMEOUT = 4, 5, 6
 PKV_F16, PKV_BF16, PKV_FP8_E4M3, PKV_F32, PKV_FP8_E4M3_TOKEN = 0, 1, 2, 3, 4
 PKV_STEP_OVERLAP = 1
+PKV_ROPE_INTERLEAVED = 1
 
 EXPORTED_SYMBOLS = (
     "pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_attention",
     "pkv_decode_step", "pkv_kv_bytes_per_token", "pkv_status_string", "pkv_version",
     "pkv_paged_decode_attention_noalloc", "pkv_copy_blocks", "pkv_paged_decode_attention_multi",
     "pkv_paged_decode_attention_window", "pkv_decode_step_fused", "pkv_paged_prefill_attention",
-    "pkv_decode_workspace_bytes_multi",
+    "pkv_decode_workspace_bytes_multi", "pkv_kv_append_rope",
+    "pkv_paged_decode_attention_biased", "pkv_paged_prefill_attention_biased",
+    "pkv_paged_decode_attention_shared_prefix", "pkv_shared_prefix_workspace_bytes",
 )
 PKV_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -141,6 +156,23 @@ def load_library():
         lib.pkv_paged_decode_attention_window.argtypes = [D, P, P, P, P, P, I32, I32, I32, I32,
                                                           I32, I32, ctypes.c_float, P, I32, I32,
                                                           P, SZ, P]
+        lib.pkv_kv_append_rope.restype = I32
+        I64 = ctypes.c_int64
+        lib.pkv_kv_append_rope.argtypes = [D, P, P, P, P, P, I32, I32, P, I64, P, I64, P, I64, P,
+                                           I32, I32, I32, P]
+        F = ctypes.c_float
+        lib.pkv_paged_decode_attention_biased.restype = I32
+        lib.pkv_paged_decode_attention_biased.argtypes = [D, P, P, P, P, P, I32, I32, I32, F, P,
+                                                          I32, I32, F, P, I32, I32, P, SZ, P]
+        lib.pkv_paged_prefill_attention_biased.restype = I32
+        lib.pkv_paged_prefill_attention_biased.argtypes = [D, P, P, P, P, P, P, I32, I32, I32,
+                                                           I32, F, F, P, P, I32, I32, P]
+        lib.pkv_shared_prefix_workspace_bytes.restype = SZ
+        lib.pkv_shared_prefix_workspace_bytes.argtypes = [D, I32, I32, I32, I32]
+        lib.pkv_paged_decode_attention_shared_prefix.restype = I32
+        lib.pkv_paged_decode_attention_shared_prefix.argtypes = [D, P, P, P, P, I32, P, P, I32,
+                                                                 I32, I32, F, P, I32, I32, P, SZ,
+                                                                 P]
         lib.pkv_copy_blocks.restype = I32
         lib.pkv_copy_blocks.argtypes = [D, P, P, P, P, I32, P]
         lib.pkv_kv_bytes_per_token.restype = U64
@@ -167,6 +199,19 @@ def _dev_ptr(t: Optional[torch.Tensor], name: str):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _row_ptr(t: torch.Tensor, name: str):
+    """Pointer and token stride of a [tokens][heads][d] tensor whose tokens may
+    lie apart (a part of a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][d]")
+    T, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0)) if T > 1 else H * d
 
 
 def _stream_handle(stream, device) -> ctypes.c_void_p:
@@ -213,6 +258,39 @@ def pkv_kv_append(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Tensor,
                            _dev_ptr(k, "k"), _dev_ptr(v, "v"), int(k.shape[0]),
                            _DTYPE_CODE.get(k.dtype, -1), _stream_handle(stream, k.device))
     _check(st, "pkv_kv_append")
+
+
+def pkv_kv_append_rope(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       slot_mapping: torch.Tensor, positions: torch.Tensor,
+                       cos_sin: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       q_out: torch.Tensor, interleaved: bool = False, stream=None) -> None:
+    """q: [T][Hq][d], k, v: [T][Hkv][d] (fp16/bf16), the tokens of each at any
+    stride; slot_mapping, positions: int64 [T]; cos_sin: fp32
+    [max_position][rot_dim], a position's cosines then its sines; q_out:
+    [T][Hq][d], which may be q."""
+    lib = load_library()
+    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
+        raise ValueError("slot_mapping and positions must be int64")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be fp32 [max_position][rot_dim]")
+    if q.dtype != k.dtype or k.dtype != v.dtype or q_out.dtype != q.dtype:
+        raise ValueError("q, k, v and q_out must have one type")
+    if k.shape != v.shape or q_out.shape != q.shape:
+        raise ValueError("k and v, and q and q_out, must have one shape")
+    T = int(k.shape[0])
+    want = ((T, desc.num_q_heads, desc.head_dim), (T, desc.num_kv_heads, desc.head_dim))
+    if tuple(q.shape) != want[0] or tuple(k.shape) != want[1]:
+        raise ValueError("q must be [T][Hq][d], k and v [T][Hkv][d]")
+    if slot_mapping.numel() != T or positions.numel() != T:
+        raise ValueError("slot_mapping and positions need one entry per token")
+    (qp, qs), (kp, ks), (vp, vs) = _row_ptr(q, "q"), _row_ptr(k, "k"), _row_ptr(v, "v")
+    st = lib.pkv_kv_append_rope(
+        ctypes.byref(desc), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+        _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(positions, "positions"),
+        _dev_ptr(cos_sin, "cos_sin"), int(cos_sin.shape[0]), int(cos_sin.shape[1]), qp, qs, kp,
+        ks, vp, vs, _dev_ptr(q_out, "q_out"), T, _DTYPE_CODE.get(q.dtype, -1),
+        PKV_ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream, q.device))
+    _check(st, "pkv_kv_append_rope")
 
 
 def pkv_copy_blocks(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -315,6 +393,86 @@ def pkv_paged_decode_attention_window(desc: CacheDesc, q: torch.Tensor, k_cache:
     _check(st, "pkv_paged_decode_attention_window")
 
 
+def _check_slopes(alibi_slopes: Optional[torch.Tensor], desc: CacheDesc) -> None:
+    if alibi_slopes is not None:
+        if alibi_slopes.dtype != torch.float32 or alibi_slopes.numel() != desc.num_q_heads:
+            raise ValueError("alibi_slopes must be fp32 with one entry per query head")
+
+
+def pkv_paged_decode_attention_biased(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,
+                                      v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                      context_lens: torch.Tensor, scale: float,
+                                      out: torch.Tensor, workspace: torch.Tensor,
+                                      softcap: float = 0.0,
+                                      alibi_slopes: Optional[torch.Tensor] = None,
+                                      window: int = 0, sinks: int = 0,
+                                      max_context_len_hint: int = 0, stream=None) -> None:
+    """As pkv_paged_decode_attention, a score s becoming softcap tanh(s /
+    softcap) (softcap > 0), then s + alibi_slopes[hq] (u - t) (fp32 [Hq]; key
+    position u, query position t); window and sinks as for the windowed call."""
+    lib = load_library()
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must be [B][Hq][d]")
+    _check_slopes(alibi_slopes, desc)
+    B, mbs = int(block_tables.shape[0]), int(block_tables.shape[1])
+    if q.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("q, block_tables and context_lens need one row per sequence")
+    st = lib.pkv_paged_decode_attention_biased(
+        ctypes.byref(desc), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables"),
+        _dev_ptr(context_lens, "context_lens"), B, int(window), int(sinks), float(softcap),
+        _dev_ptr(alibi_slopes, "alibi_slopes"), mbs, int(max_context_len_hint), float(scale),
+        _dev_ptr(out, "out"), _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
+        _dev_ptr(workspace, "workspace"), int(workspace.numel() * workspace.element_size()),
+        _stream_handle(stream, q.device))
+    _check(st, "pkv_paged_decode_attention_biased")
+
+
+def pkv_shared_prefix_workspace_bytes(desc: CacheDesc, batch: int, num_prefix_blocks: int,
+                                      max_blocks_per_seq: int,
+                                      max_context_len_hint: int = 0) -> int:
+    lib = load_library()
+    return int(lib.pkv_shared_prefix_workspace_bytes(ctypes.byref(desc), int(batch),
+                                                     int(num_prefix_blocks),
+                                                     int(max_blocks_per_seq),
+                                                     int(max_context_len_hint)))
+
+
+def pkv_paged_decode_attention_shared_prefix(desc: CacheDesc, q: torch.Tensor,
+                                             k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                             prefix_blocks: torch.Tensor,
+                                             block_tables: torch.Tensor,
+                                             context_lens: torch.Tensor, scale: float,
+                                             out: torch.Tensor, workspace: torch.Tensor,
+                                             max_context_len_hint: int = 0,
+                                             stream=None) -> None:
+    """As pkv_paged_decode_attention for sequences that all begin with the
+    blocks prefix_blocks (int32 [num_prefix_blocks]), which are read once for
+    the batch; block_tables holds whole tables, whose entries for the prefix
+    are not read, and context_lens whole lengths."""
+    lib = load_library()
+    for t, n in ((prefix_blocks, "prefix_blocks"), (block_tables, "block_tables"),
+                 (context_lens, "context_lens")):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{n} must be int32")
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must be [B][Hq][d]")
+    B, mbs = int(block_tables.shape[0]), int(block_tables.shape[1])
+    if q.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("q, block_tables and context_lens need one row per sequence")
+    st = lib.pkv_paged_decode_attention_shared_prefix(
+        ctypes.byref(desc), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache"), _dev_ptr(prefix_blocks, "prefix_blocks"),
+        int(prefix_blocks.numel()), _dev_ptr(block_tables, "block_tables"),
+        _dev_ptr(context_lens, "context_lens"), B, mbs, int(max_context_len_hint), float(scale),
+        _dev_ptr(out, "out"), _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
+        _dev_ptr(workspace, "workspace"), int(workspace.numel() * workspace.element_size()),
+        _stream_handle(stream, q.device))
+    _check(st, "pkv_paged_decode_attention_shared_prefix")
+
+
 def pkv_decode_step(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,
                     v_cache: torch.Tensor, slot_mapping: torch.Tensor, k: torch.Tensor,
                     v: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -366,6 +524,37 @@ def pkv_paged_prefill_attention(desc: CacheDesc, q: torch.Tensor, k_cache: torch
         _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
         _stream_handle(stream, q.device))
     _check(st, "pkv_paged_prefill_attention")
+
+
+def pkv_paged_prefill_attention_biased(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,
+                                       v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                       context_lens: torch.Tensor, q_start: torch.Tensor,
+                                       max_q_len: int, scale: float, out: torch.Tensor,
+                                       softcap: float = 0.0,
+                                       alibi_slopes: Optional[torch.Tensor] = None,
+                                       stream=None) -> None:
+    """As pkv_paged_prefill_attention, the scores changed as by
+    pkv_paged_decode_attention_biased (t the row's position)."""
+    lib = load_library()
+    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
+                 (q_start, "q_start")):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{n} must be int32")
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must be [total_q][Hq][d]")
+    _check_slopes(alibi_slopes, desc)
+    B, mbs = int(block_tables.shape[0]), int(block_tables.shape[1])
+    if q_start.numel() != B + 1 or context_lens.numel() != B:
+        raise ValueError("q_start needs batch + 1 entries and context_lens batch")
+    st = lib.pkv_paged_prefill_attention_biased(
+        ctypes.byref(desc), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables"),
+        _dev_ptr(context_lens, "context_lens"), _dev_ptr(q_start, "q_start"), B,
+        int(q.shape[0]), int(max_q_len), mbs, float(scale), float(softcap),
+        _dev_ptr(alibi_slopes, "alibi_slopes"), _dev_ptr(out, "out"),
+        _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
+        _stream_handle(stream, q.device))
+    _check(st, "pkv_paged_prefill_attention_biased")
 
 
 def pkv_decode_step_fused(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,

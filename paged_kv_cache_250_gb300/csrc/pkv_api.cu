@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <math.h>
 
 #include <atomic>
 #include <mutex>
@@ -176,6 +177,87 @@ pkv_status encode_cache_map(CUtensorMap* map, const void* cache, const pkv_cache
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// Query rows [rows][Hq][d] in boxes of 128 / g rows x the g heads of a KV head.
+pkv_status encode_q_map(CUtensorMap* map, const void* q, const pkv_cache_desc* desc,
+                        int32_t rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return PKV_ERR_CUDA;
+  const cuuint64_t hd = (cuuint64_t)desc->head_dim;
+  const cuuint64_t dims[3] = {hd, (cuuint64_t)desc->num_q_heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {hd * 2, (cuuint64_t)desc->num_q_heads * hd * 2};
+  const int G = desc->num_q_heads / desc->num_kv_heads;
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
+// A cap is 0 (none) or between 2^-10 and 2^20: far outside the scores any
+// softmax separates, 2 / cap and the cap itself stay well inside fp32.
+pkv_status bias_checks(float softcap, const float* slopes) {
+  if (softcap != 0.f && !(softcap >= 0x1p-10f && softcap <= 0x1p20f)) return PKV_ERR_INVALID_ARG;
+  if (!aligned(slopes, 4)) return PKV_ERR_INVALID_ARG;
+  return PKV_OK;
+}
+
+// Shared prefix: the front of the workspace.  Sizes grow with the batch alone
+// (the partials of at most kPrefixItems CTAs, or of one per pair of row tiles
+// when there are more pairs), so a workspace for a batch serves smaller ones.
+struct SharedLayout {
+  size_t lse_off, own_off, ml_off, o_off, total;
+  int32_t pairs;
+};
+constexpr int64_t kPrefixItemsPerSm = 2;
+SharedLayout shared_layout(const pkv_cache_desc* d, int32_t batch, int sms) {
+  const int64_t rows = (int64_t)batch * (d->num_q_heads / d->num_kv_heads);
+  SharedLayout s;
+  s.pairs = (int32_t)((rows + 255) / 256);
+  const int64_t least = (int64_t)s.pairs * d->num_kv_heads;
+  const int64_t items = least > kPrefixItemsPerSm * sms ? least : kPrefixItemsPerSm * sms;
+  const int64_t outs = (int64_t)batch * d->num_q_heads;
+  s.lse_off = 0;
+  s.own_off = align256(outs * sizeof(float));
+  s.ml_off = align256(s.own_off + outs * d->head_dim * sizeof(float));
+  s.o_off = align256(s.ml_off + items * 256 * 2 * sizeof(float));
+  s.total = align256(s.o_off + items * 256 * d->head_dim * sizeof(float));
+  return s;
+}
+
+// CTAs the blocks of a pair of row tiles are cut over: the count that makes
+// the longest SM's work least, at kBlockCost per block (of 128 tokens) a CTA
+// takes and kCtaCost for its start and end.
+int32_t shared_splits(const pkv_cache_desc* d, int32_t batch, int32_t npb, const SharedLayout& s,
+                      int sms) {
+  constexpr int64_t kBlockCost = 2, kCtaCost = 5;
+  const int64_t least = (int64_t)s.pairs * d->num_kv_heads;
+  const int64_t nblk = ((int64_t)npb * kPageSize + 127) / 128;
+  int64_t most = kPrefixItemsPerSm * sms / least;
+  if (most > nblk) most = nblk;
+  (void)batch;
+  int32_t best = 1;
+  int64_t best_cost = -1;
+  for (int64_t n = 1; n <= most; ++n) {
+    const int64_t waves = (least * n + sms - 1) / sms;
+    const int64_t cost = waves * (kBlockCost * ((nblk + n - 1) / n) + kCtaCost);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = (int32_t)n;
+    }
+  }
+  return best;
+}
+
+// Whether the prefix is worth a pass of its own; otherwise every sequence reads
+// it through the prefix table, one launch in place of three.
+bool shared_pays(const pkv_cache_desc* d, int32_t batch, int32_t npb) {
+  (void)d;
+  return batch > 1 && npb > 0;
+}
+
 pkv_status append_checks(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,
                          const int64_t* slot_mapping, const void* k, const void* v,
                          int32_t num_tokens, pkv_dtype kv_dtype) {
@@ -245,6 +327,17 @@ pkv_status decode_validate(const pkv_cache_desc* desc, const void* q, const void
 
 namespace {
 
+// What the biased and shared-prefix forms of the single-token kernel add.
+struct DecodeForm {
+  int mode = pkv::kModePlain;
+  float softcap = 0.f;
+  const float* slopes = nullptr;
+  const int32_t* prefix_blocks = nullptr;
+  int32_t npb = 0;
+  int32_t skip_prefix = 0;
+  float* lse = nullptr;
+};
+
 pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_cache,
                        const void* v_cache, const int32_t* block_tables,
                        const int32_t* context_lens, int32_t batch, int32_t max_blocks_per_seq,
@@ -253,14 +346,21 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
                        pkv_stream_t stream, int early_prologue, int32_t qlen = 1,
                        int32_t window = 0, int32_t sinks = 0, const void* k_new = nullptr,
                        const void* v_new = nullptr, pkv_dtype kv_dtype = PKV_BF16,
-                       int trigger_next = 0) {
+                       int trigger_next = 0, const DecodeForm& form = DecodeForm()) {
   pkv_status st = decode_checks(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
                                 max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype,
                                 out_dtype, workspace, workspace_bytes, qlen);
   if (st != PKV_OK || batch == 0) return st;
   const int sms = sm_count_current_device();
-  const WsLayout w =
+  WsLayout w =
       ws_layout(desc, batch, max_blocks_per_seq, max_context_len_hint, sms, nc_of(desc, qlen));
+  if (form.skip_prefix) {  // fewer units; the layout is the same
+    const int32_t skip = form.npb * kPageSize;
+    const int32_t hint = max_context_len_hint > skip ? max_context_len_hint - skip : 0;
+    w.ctas = ws_layout(desc, batch, max_blocks_per_seq - form.npb,
+                       max_context_len_hint > 0 && hint == 0 ? 1 : hint, sms,
+                       nc_of(desc, qlen)).ctas;
+  }
   pkv::DecodeLaunch l;
   st = encode_cache_map(&l.tmap_k, k_cache, desc);
   if (st != PKV_OK) return st;
@@ -295,6 +395,13 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
   l.p.kv_bf16 = kv_dtype == PKV_BF16 ? 1 : 0;
   l.p.sinks = window > 0 ? sinks : 0;
   l.p.scale_log2 = scale * 1.4426950408889634f;
+  l.p.cap_log2 = form.softcap * 1.4426950408889634f;
+  l.p.cap_z = form.softcap > 0.f ? 2.f / form.softcap : 0.f;
+  l.p.slopes = form.slopes;
+  l.p.prefix_blocks = form.prefix_blocks;
+  l.p.npb = form.npb;
+  l.p.skip_prefix = form.skip_prefix;
+  l.p.lse = form.lse;
   l.group = desc->num_q_heads / desc->num_kv_heads;
   // query-token capacity of the kernel: 1, or the smallest of 2, 4, 8 that
   // holds qlen
@@ -304,7 +411,17 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
   l.ctas = w.ctas;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (l.qcap == 1) {
+  if (form.mode == pkv::kModeShared) {
+    e = l.cache == pkv::kCacheF16 ? pkv::launch_decode_shared_f16(l)
+                                  : pkv::launch_decode_shared_bf16(l);
+  } else if (form.mode == pkv::kModeBiased) {
+    switch (l.cache) {
+      case pkv::kCacheF16: e = pkv::launch_decode_biased_f16(l); break;
+      case pkv::kCacheBF16: e = pkv::launch_decode_biased_bf16(l); break;
+      case pkv::kCacheE4M3: e = pkv::launch_decode_biased_e4m3(l); break;
+      default: e = pkv::launch_decode_biased_e4m3_tok(l); break;
+    }
+  } else if (l.qcap == 1) {
     switch (l.cache) {
       case pkv::kCacheF16: e = pkv::launch_decode_f16(l); break;
       case pkv::kCacheBF16: e = pkv::launch_decode_bf16(l); break;
@@ -357,6 +474,60 @@ pkv_status pkv_kv_append(const pkv_cache_desc* desc, void* k_cache, void* v_cach
   a.NB = desc->num_blocks;
   cudaError_t e = pkv::launch_append(a, kind_of(desc->cache_dtype), kv_dtype == PKV_BF16,
                                      reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_append_rope(const pkv_cache_desc* desc, void* k_cache, void* v_cache,
+                              const int64_t* slot_mapping, const int64_t* positions,
+                              const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, void* q_out, int32_t num_tokens,
+                              pkv_dtype dtype, int32_t flags, pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || (flags & ~PKV_ROPE_INTERLEAVED) != 0) return PKV_ERR_INVALID_ARG;
+  if (rot_dim <= 0 || rot_dim > desc->head_dim || max_position <= 0) return PKV_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PKV_OK;
+  st = append_checks(desc, k_cache, v_cache, slot_mapping, k, v, num_tokens, dtype);
+  if (st != PKV_OK) return st;
+  if (!positions || !cos_sin || !q || !q_out) return PKV_ERR_INVALID_ARG;
+  if (!aligned(positions, 8) || !aligned(cos_sin, 16) || !aligned(q, 16) || !aligned(q_out, 16))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t qrow = (int64_t)desc->num_q_heads * desc->head_dim;
+  const int64_t kvrow = (int64_t)desc->num_kv_heads * desc->head_dim;
+  if (q_stride < qrow || k_stride < kvrow || v_stride < kvrow) return PKV_ERR_INVALID_ARG;
+  if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0) return PKV_ERR_INVALID_ARG;
+  pkv::RopeParams p;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.k_scale = desc->k_scale;
+  p.v_scale = desc->v_scale;
+  p.scale_out = nullptr;
+  if (desc->cache_dtype == PKV_FP8_E4M3_TOKEN) p.scale_out = const_cast<float*>(desc->k_scale);
+  p.err_word = desc->err_word;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.T = num_tokens;
+  p.Hq = desc->num_q_heads;
+  p.Hkv = desc->num_kv_heads;
+  p.d = desc->head_dim;
+  p.NB = desc->num_blocks;
+  p.rot = rot_dim;
+  p.max_position = max_position;
+  p.interleaved = (flags & PKV_ROPE_INTERLEAVED) ? 1 : 0;
+  const cudaError_t e =
+      pkv::launch_rope_append(p, kind_of(desc->cache_dtype), dtype == PKV_BF16,
+                              reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -471,14 +642,128 @@ pkv_status pkv_decode_step(const pkv_cache_desc* desc, const void* q, void* k_ca
                      workspace, workspace_bytes, stream, /*early_prologue=*/1);
 }
 
-pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* desc, const void* q,
-                                       const void* k_cache, const void* v_cache,
-                                       const int32_t* block_tables,
-                                       const int32_t* context_lens, const int32_t* q_start,
-                                       int32_t batch, int32_t total_q, int32_t max_q_len,
-                                       int32_t max_blocks_per_seq, float scale, void* out,
-                                       pkv_dtype q_dtype, pkv_dtype out_dtype,
-                                       pkv_stream_t stream) {
+pkv_status pkv_paged_decode_attention_biased(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, int32_t batch, int32_t window,
+    int32_t sinks, float softcap, const float* alibi_slopes, int32_t max_blocks_per_seq,
+    int32_t max_context_len_hint, float scale, void* out, pkv_dtype q_dtype, pkv_dtype out_dtype,
+    void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if (window < 0 || sinks < 0) return PKV_ERR_INVALID_ARG;
+  st = bias_checks(softcap, alibi_slopes);
+  if (st != PKV_OK) return st;
+  DecodeForm form;
+  if (softcap > 0.f || alibi_slopes != nullptr) form.mode = pkv::kModeBiased;
+  form.softcap = softcap;
+  form.slopes = alibi_slopes;
+  return decode_impl(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
+                     max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype, out_dtype,
+                     workspace, workspace_bytes, stream, /*early_prologue=*/0, 1, window, sinks,
+                     nullptr, nullptr, PKV_BF16, 0, form);
+}
+
+size_t pkv_shared_prefix_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                         int32_t num_prefix_blocks, int32_t max_blocks_per_seq,
+                                         int32_t max_context_len_hint) {
+  if (check_desc(desc) != PKV_OK || is_fp8(desc->cache_dtype)) return 0;
+  if (num_prefix_blocks < 0 || num_prefix_blocks > max_blocks_per_seq) return 0;
+  const size_t own =
+      pkv_decode_workspace_bytes(desc, batch, max_blocks_per_seq, max_context_len_hint);
+  const int sms = sm_count_current_device();
+  return own == 0 || sms <= 0 ? 0 : shared_layout(desc, batch, sms).total + own;
+}
+
+pkv_status pkv_paged_decode_attention_shared_prefix(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* prefix_blocks, int32_t num_prefix_blocks, const int32_t* block_tables,
+    const int32_t* context_lens, int32_t batch, int32_t max_blocks_per_seq,
+    int32_t max_context_len_hint, float scale, void* out, pkv_dtype q_dtype, pkv_dtype out_dtype,
+    void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if (is_fp8(desc->cache_dtype)) return PKV_ERR_UNSUPPORTED;
+  if (num_prefix_blocks < 0 || num_prefix_blocks > max_blocks_per_seq) return PKV_ERR_INVALID_ARG;
+  if (!(scale > 0.f)) return PKV_ERR_INVALID_ARG;  // row maxima are taken unscaled
+  if (batch > 0 && num_prefix_blocks > 0 && (!prefix_blocks || !aligned(prefix_blocks, 4)))
+    return PKV_ERR_INVALID_ARG;
+  const int sms = sm_count_current_device();
+  const SharedLayout s = shared_layout(desc, batch > 0 ? batch : 1, sms > 0 ? sms : 1);
+  char* ws = static_cast<char*>(workspace);
+  char* own = workspace_bytes > s.total && ws != nullptr ? ws + s.total : nullptr;
+  const size_t own_bytes = own != nullptr ? workspace_bytes - s.total : 0;
+  st = decode_checks(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
+                     max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype, out_dtype,
+                     own, own_bytes);
+  if (st != PKV_OK || batch == 0) return st;
+  DecodeForm form;
+  form.mode = pkv::kModeShared;
+  form.prefix_blocks = prefix_blocks;
+  form.npb = num_prefix_blocks;
+  if (!shared_pays(desc, batch, num_prefix_blocks))
+    return decode_impl(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
+                       max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype, out_dtype,
+                       own, own_bytes, stream, /*early_prologue=*/0, 1, 0, 0, nullptr, nullptr,
+                       PKV_BF16, 0, form);
+  // the prefix for all rows at once, then each sequence's own part, then the merge
+  pkv::PrefixLaunch l;
+  st = encode_cache_map(&l.tmap_k, k_cache, desc);
+  if (st != PKV_OK) return st;
+  st = encode_cache_map(&l.tmap_v, v_cache, desc);
+  if (st != PKV_OK) return st;
+  st = encode_q_map(&l.tmap_q, q, desc, batch);
+  if (st != PKV_OK) return st;
+  l.p.context_lens = context_lens;
+  l.p.prefix_blocks = prefix_blocks;
+  l.p.part_ml = reinterpret_cast<float*>(ws + s.ml_off);
+  l.p.part_o = reinterpret_cast<float*>(ws + s.o_off);
+  l.p.err_word = desc->err_word;
+  l.p.B = batch;
+  l.p.Hq = desc->num_q_heads;
+  l.p.Hkv = desc->num_kv_heads;
+  l.p.NB = desc->num_blocks;
+  l.p.MBS = max_blocks_per_seq;
+  l.p.npb = num_prefix_blocks;
+  l.p.pairs = s.pairs;
+  l.p.splits = shared_splits(desc, batch, num_prefix_blocks, s, sms);
+  l.p.scale_log2 = scale * 1.4426950408889634f;
+  l.bf16 = desc->cache_dtype == PKV_BF16;
+  l.d = desc->head_dim;
+  l.stream = reinterpret_cast<cudaStream_t>(stream);
+  if (pkv::launch_prefix(l) != cudaSuccess) return PKV_ERR_CUDA;
+  form.skip_prefix = 1;
+  form.lse = reinterpret_cast<float*>(ws + s.lse_off);
+  float* own_o = reinterpret_cast<float*>(ws + s.own_off);
+  st = decode_impl(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
+                   max_blocks_per_seq, max_context_len_hint, scale, own_o, q_dtype, PKV_F32, own,
+                   own_bytes, stream, /*early_prologue=*/0, 1, 0, 0, nullptr, nullptr, PKV_BF16,
+                   0, form);
+  if (st != PKV_OK) return st;
+  pkv::PrefixMergeParams m;
+  m.part_o = l.p.part_o;
+  m.part_ml = l.p.part_ml;
+  m.own_o = own_o;
+  m.lse = form.lse;
+  m.out = out;
+  m.B = batch;
+  m.Hq = desc->num_q_heads;
+  m.Hkv = desc->num_kv_heads;
+  m.pairs = s.pairs;
+  m.splits = l.p.splits;
+  m.out_dtype = out_dtype;
+  return pkv::launch_prefix_merge(m, desc->head_dim, l.stream) == cudaSuccess ? PKV_OK
+                                                                              : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const void* k_cache,
+                        const void* v_cache, const int32_t* block_tables,
+                        const int32_t* context_lens, const int32_t* q_start, int32_t batch,
+                        int32_t total_q, int32_t max_q_len, int32_t max_blocks_per_seq,
+                        float scale, float softcap, const float* slopes, void* out,
+                        pkv_dtype q_dtype, pkv_dtype out_dtype, pkv_stream_t stream) {
   pkv_status st = check_desc(desc);
   if (st != PKV_OK) return st;
   if (batch < 0 || total_q < 0 || max_q_len < 0 || max_blocks_per_seq <= 0)
@@ -503,18 +788,9 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* desc, const void* q
   if (st != PKV_OK) return st;
   st = encode_cache_map(&l.tmap_v, v_cache, desc);
   if (st != PKV_OK) return st;
-  auto fn = encode_fn();
-  if (fn == nullptr) return PKV_ERR_CUDA;
-  const cuuint64_t hd = (cuuint64_t)desc->head_dim;
-  const cuuint64_t dims[3] = {hd, (cuuint64_t)desc->num_q_heads, (cuuint64_t)total_q};
-  const cuuint64_t strides[2] = {hd * 2, (cuuint64_t)desc->num_q_heads * hd * 2};
-  const int G = desc->num_q_heads / desc->num_kv_heads;  // a box: 128 / G tokens x G heads
-  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  if (fn(&l.tmap_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(q), dims, strides, box,
-         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return PKV_ERR_CUDA;
+  st = encode_q_map(&l.tmap_q, q, desc, total_q);
+  if (st != PKV_OK) return st;
+  const int G = desc->num_q_heads / desc->num_kv_heads;
   l.p.q_start = q_start;
   l.p.context_lens = context_lens;
   l.p.block_tables = block_tables;
@@ -529,11 +805,49 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* desc, const void* q
   l.p.tiles_per_seq = (max_q_len + 256 / G - 1) / (256 / G);  // a CTA: 256 / G tokens
   l.p.out_dtype = out_dtype;
   l.p.scale_log2 = scale * 1.4426950408889634f;
+  l.p.cap_log2 = softcap * 1.4426950408889634f;
+  l.p.cap_z = softcap > 0.f ? l.p.scale_log2 * (2.f / softcap) : 0.f;
+  l.p.slopes = slopes;
+  l.p.cap_fine = softcap > pkv::kCapCoarse ? 1 : 0;
+  if (!(l.p.cap_z < INFINITY)) return PKV_ERR_INVALID_ARG;
   l.bf16 = desc->cache_dtype == PKV_BF16;
   l.d = desc->head_dim;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
   if ((int64_t)batch * l.p.tiles_per_seq >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
-  return pkv::launch_prefill(l) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  const cudaError_t e = softcap > 0.f || slopes != nullptr ? pkv::launch_prefill_biased(l)
+                                                           : pkv::launch_prefill(l);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* desc, const void* q,
+                                       const void* k_cache, const void* v_cache,
+                                       const int32_t* block_tables,
+                                       const int32_t* context_lens, const int32_t* q_start,
+                                       int32_t batch, int32_t total_q, int32_t max_q_len,
+                                       int32_t max_blocks_per_seq, float scale, void* out,
+                                       pkv_dtype q_dtype, pkv_dtype out_dtype,
+                                       pkv_stream_t stream) {
+  return prefill_impl(desc, q, k_cache, v_cache, block_tables, context_lens, q_start, batch,
+                      total_q, max_q_len, max_blocks_per_seq, scale, 0.f, nullptr, out, q_dtype,
+                      out_dtype, stream);
+}
+
+pkv_status pkv_paged_prefill_attention_biased(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_start,
+    int32_t batch, int32_t total_q, int32_t max_q_len, int32_t max_blocks_per_seq, float scale,
+    float softcap, const float* alibi_slopes, void* out, pkv_dtype q_dtype, pkv_dtype out_dtype,
+    pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  st = bias_checks(softcap, alibi_slopes);
+  if (st != PKV_OK) return st;
+  return prefill_impl(desc, q, k_cache, v_cache, block_tables, context_lens, q_start, batch,
+                      total_q, max_q_len, max_blocks_per_seq, scale, softcap, alibi_slopes, out,
+                      q_dtype, out_dtype, stream);
 }
 
 pkv_status pkv_decode_step_fused(const pkv_cache_desc* desc, const void* q, void* k_cache,

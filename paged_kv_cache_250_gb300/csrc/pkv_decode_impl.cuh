@@ -61,6 +61,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -140,12 +142,18 @@ __device__ __forceinline__ void store_out_rt(pkv_dtype t, void* base, int64_t id
 // The library builds it for one query token (QC = 1); several query tokens
 // per sequence go to the kernel of pkv_decode_mq.cuh.  DEEP: the deeper ring
 // and barrier-tree segment ends of the per-token E4M3 kernel at small batches.
-template <int D, int G, int QC, int CACHE, bool QBF16, bool DEEP>
+// MODE: kModeBiased caps the scores by a tanh and / or adds a bias that grows
+// with the distance, a handful of instructions on the four scores a lane holds
+// of a page; kModeShared reads a prefix that all sequences share through its
+// own table, or leaves it out and writes each row's log2 sum for the merge.
+template <int D, int G, int QC, int CACHE, bool QBF16, bool DEEP, int MODE>
 __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCtasPerSm)
     decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
   constexpr int NC = G * QC;
   static_assert(NC <= 8, "one MMA column per (query token, head)");
+  constexpr bool kBiased = MODE == kModeBiased, kShared = MODE == kModeShared;
+  static_assert(MODE == kModePlain || QC == 1, "built for one query token");
   using C = DecodeCfg<D, CACHE, DEEP>;
   constexpr bool kBF = (CACHE == kCacheBF16);  // mma operand type (else fp16)
   constexpr int kS = C::kStages;
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // only (E4M3 steps enqueue the append kernel first)
   constexpr bool kFp8 = cache_is_fp8((CacheKind)CACHE);
   constexpr bool kTok = CACHE == kCacheE4M3Tok;  // one scale per token and KV head
-  constexpr bool kFusedAppend = QC == 1 && !kFp8;
+  constexpr bool kFusedAppend = QC == 1 && !kFp8 && MODE == kModePlain;
 
   // the next kernel on the stream may launch (a programmatic dependent waits
   // for this one to complete before it reads what this one writes)
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
-  if (!p.early_prologue) griddep_wait();
+  if (!p.early_prologue && !(kShared && p.skip_prefix)) griddep_wait();
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -228,11 +236,17 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
         sk = fw - nsp;
       }
     }
+    if constexpr (kShared) {  // the prefix is a gap before the sequence's first unit
+      if (p.skip_prefix) {
+        ns = 0;
+        sk = min(np, p.npb);
+      }
+    }
     ctxs[b] = c;
     gns[b] = ns;
     gsk[b] = sk;
     pfx[b + 1] = np - sk;
-    nzp[b + 1] = np > 0 ? 1 : 0;
+    nzp[b + 1] = np - (kShared ? sk : 0) > 0 ? 1 : 0;
   }
   if (lane == 0) {
     for (int s = 0; s < kS; ++s) mbar_init(smem_u32(&bars[warp * kS + s]), 1);
@@ -348,6 +362,13 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     }
     return y;
   };
+  // the block of page pg of sequence b
+  auto block_of = [&](int b, int pg) -> int {
+    if constexpr (kShared) {
+      if (pg < p.npb) return p.prefix_blocks[pg];
+    }
+    return p.block_tables[(int64_t)b * p.MBS + pg];
+  };
   auto fill_desc = [&](int2 r, int ord0) {  // {tma row or -1, page_info}
     const int cnt = warp_count(r);
     for (int j = lane; j < cnt; j += 32) {
@@ -358,7 +379,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       const int h = (int)udiv64(rr, np);
       const int pgu = (int)(rr - (int64_t)h * np);  // unit within the segment
       const int pg = pgu < gns[b] ? pgu : pgu + gsk[b];
-      const int blk = p.block_tables[(int64_t)b * p.MBS + pg];
+      const int blk = block_of(b, pg);
       int row = -1;
       if (blk >= 0 && blk < p.NB) row = (blk * p.Hkv + h) * kPageSize;
       else report_error(p.err_word, PKV_ERR_BOUNDS);
@@ -392,7 +413,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       f_h = (int)udiv64(rr, np);
       const int pgu = (int)(rr - (int64_t)f_h * np);  // unit within the segment
       const int pg = pgu < gns[b] ? pgu : pgu + gsk[b];
-      f_blk = p.block_tables[(int64_t)b * p.MBS + pg];
+      f_blk = block_of(b, pg);
       f_valid = page_info(b, pg);
       if (lane == 0 || pgu == 0) {  // a segment may start here: warm its q rows in L2
         for (int i = 0; i < p.qlen; ++i) {
@@ -482,6 +503,10 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     const int64_t row0 = (int64_t)b * p.qlen * p.Hq * D;
     for (int i = tid; i < p.qlen * p.Hq * D; i += blockDim.x)
       store_out_rt(p.out_dtype, p.out, row0 + i, 0.f);
+    if constexpr (kShared) {
+      if (p.skip_prefix)
+        for (int i = tid; i < p.Hq; i += blockDim.x) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
+    }
   }
 
   // ---- per-lane fragment coordinates
@@ -504,6 +529,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // score scale in log2 units (E4M3: times the K scale) for the lane's two
   // C-fragment columns 2 c4 and 2 c4 + 1
   float c2a = 0.f, c2b = 0.f;
+  float sla = 0.f, slb = 0.f;  // kModeBiased: the same two columns' slopes, log2 units
 
   auto reset_state = [&]() {
 #pragma unroll
@@ -522,6 +548,13 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   auto col_real = [&](int c) -> bool { return c < NC && c < G * p.qlen; };
 
   auto load_q = [&](int b, int h) {
+    if constexpr (kBiased) {
+      if (p.slopes != nullptr) {
+        constexpr float kLog2e = 1.4426950408889634f;
+        sla = col_real(2 * c4) ? p.slopes[h * G + 2 * c4] * kLog2e : 0.f;
+        slb = col_real(2 * c4 + 1) ? p.slopes[h * G + 2 * c4 + 1] * kLog2e : 0.f;
+      }
+    }
     const int col = r8;  // B-fragment column n = lane / 4
     const bool real = col_real(col);
     const uint16_t* qrow =
@@ -663,7 +696,8 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // softmax update over all their tokens (log2 domain; tokens past the
   // context are masked), then P.V.  Several pages give the warp independent
   // MMA chains and fewer reductions per token.
-  auto compute_pages = [&](auto npc, const uint32_t* kt, const int* valids) {
+  // rels (kModeBiased): the distance of each page's first token from the query.
+  auto compute_pages = [&](auto npc, const uint32_t* kt, const int* valids, const int* rels) {
     constexpr int NP = decltype(npc)::value;
     float x[NP][4];
     float ksc[NP][2], vsc[NP][2];  // per-token K and V scales of rows r8, r8 + 8
@@ -694,6 +728,19 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
         x[i][3] *= ksc[i][1];
         if (r8 >= rem) vsc[i][0] = 0.f;  // their P is 0; their scale may be anything
         if (r8 + 8 >= rem) vsc[i][1] = 0.f;
+      }
+      if constexpr (kBiased) {
+        if (p.cap_log2 > 0.f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = cap_score(x[i][e], p.cap_z, p.cap_log2);
+        }
+        if (p.slopes != nullptr) {
+          const float da = (float)(rels[i] + r8), db = (float)(rels[i] + r8 + 8);
+          x[i][0] = fmaf(sla, da, x[i][0]);
+          x[i][1] = fmaf(slb, da, x[i][1]);
+          x[i][2] = fmaf(sla, db, x[i][2]);
+          x[i][3] = fmaf(slb, db, x[i][3]);
+        }
       }
       if constexpr (QC == 1) {
         if (rem < kPageSize) {
@@ -784,10 +831,11 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
               movm_trans(l23));
     }
   };
-  auto compute_page = [&](uint32_t kt, int valid) {
+  auto compute_page = [&](uint32_t kt, int valid, int rel) {
     const uint32_t kt1[1] = {kt};
     const int v1[1] = {valid};
-    compute_pages(Int<1>{}, kt1, v1);
+    const int r1[1] = {rel};
+    compute_pages(Int<1>{}, kt1, v1, r1);
   };
 
   // ---- fused append (16-bit caches): the page holding a sequence's newest
@@ -923,6 +971,10 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
           }
         }
       }
+      if constexpr (kShared) {
+        if (p.skip_prefix && col % (D / 4) == 0)
+          p.lse[col_row(b, h, head)] = lsum != 0.f ? M + log2f(lsum) : -INFINITY;
+      }
       const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
       const int64_t ob = col_row(b, h, head) * D + (col % (D / 4)) * 4;
       store_out_rt(p.out_dtype, p.out, ob + 0, acc.x * inv);
@@ -1018,6 +1070,12 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       const float i0 = lt0 > 0.f ? vs / lt0 : 0.f;
       const float i1 = lt1 > 0.f ? vs / lt1 : 0.f;
       const bool w0 = col_real(h0), w1 = col_real(h1);
+      if constexpr (kShared) {
+        if (p.skip_prefix && r8 == 0) {
+          if (w0) p.lse[col_row(b, h, h0)] = lt0 != 0.f ? m2[0] + log2f(lt0) : -INFINITY;
+          if (w1) p.lse[col_row(b, h, h1)] = lt1 != 0.f ? m2[1] + log2f(lt1) : -INFINITY;
+        }
+      }
       const int64_t ob0 = (w0 ? col_row(b, h, h0) : 0) * D;
       const int64_t ob1 = (w1 ? col_row(b, h, h1) : 0) * D;
 #pragma unroll
@@ -1171,6 +1229,12 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       const int64_t hi_j = pe - R.x - warp + NW - 1;
       const int j0 = (int)((lo_j > 0 ? lo_j : 0) / NW);
       const int j1 = (int)((hi_j > 0 ? hi_j : 0) / NW);
+      // kModeBiased: first token of the page of ordinal j, less the query's position
+      auto rel_of = [&](int j) -> int {
+        if constexpr (!kBiased) return 0;
+        const int pgu = (int)((int64_t)R.x + warp + (int64_t)NW * j - seg_start);
+        return (pgu < gns[b] ? pgu : pgu + gsk[b]) * kPageSize - (ctxs[b] - 1);
+      };
       for (int j = j0; j < j1; ++j, ++k) {
         if (!have_q) {
           load_q(b, h);
@@ -1180,7 +1244,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
           const int ng = (j1 - j >= kGroup) ? kGroup : 1;
           if (ng > 1) {
             uint32_t kt[kGroup];
-            int vv[kGroup], rw[kGroup];
+            int vv[kGroup], rw[kGroup], rel[kGroup];
             bool all_ok = true;
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
@@ -1193,6 +1257,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
                 kt[i] = ring + (uint32_t)(si * C::kStageBytes);
                 vv[i] = (di.x >= 0) ? di.y : 0;
                 rw[i] = di.x;
+                rel[i] = rel_of(j + i);
                 all_ok = all_ok && vv[i] > 0;
               }
             }
@@ -1206,10 +1271,10 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
             }
             if (!dead) {
               if (all_ok) {
-                compute_pages(Int<kGroup>{}, kt, vv);
+                compute_pages(Int<kGroup>{}, kt, vv, rel);
               } else {
                 for (int i = 0; i < ng; ++i)
-                  if (vv[i] > 0) compute_page(kt[i], vv[i]);
+                  if (vv[i] > 0) compute_page(kt[i], vv[i], rel[i]);
               }
             }
             __syncwarp();
@@ -1232,7 +1297,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
                        b, h);
         }
         if (!dead && dsc.x >= 0 && dsc.y > 0)
-          compute_page(ring + (uint32_t)(slot * C::kStageBytes), dsc.y);
+          compute_page(ring + (uint32_t)(slot * C::kStageBytes), dsc.y, rel_of(j));
         __syncwarp();
         if (fill_commit()) filled_end = f_ord + f_cnt;
         if (!dead) top_up(k + 1);
@@ -1256,20 +1321,30 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       mbar_wait_bounded(smem_u32(&bars[warp * kS + (q % kS)]), (uint32_t)((q / kS) & 1),
                         kWaitLimitNs);
   }
+  if constexpr (kShared) {
+    // this pass read nothing of the prefix kernel before it on the stream; the
+    // merge behind it waits for this kernel alone, so this one ends after both
+    if (p.skip_prefix) griddep_wait();
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Host-side dispatch over head_dim, group and query tokens for one cache kind.
-template <int D, int G, int QC, int CACHE, bool QBF16, bool DEEP>
+template <int D, int G, int QC, int CACHE, bool QBF16, bool DEEP, int MODE>
 cudaError_t launch_split(const DecodeLaunch& l) {
-  auto kern = decode_kernel<D, G, QC, CACHE, QBF16, DEEP>;
+  auto kern = decode_kernel<D, G, QC, CACHE, QBF16, DEEP, MODE>;
   const size_t smem = decode_smem_bytes_form(D, (CacheKind)CACHE, l.p.B, DEEP);
-  static size_t configured = 0;  // largest dynamic smem size set so far
-  if (smem > configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+  // the limit is raised once per device, to what any batch may ask for, so
+  // that calls from several threads cannot lower it under one another
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(configured.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    configured = smem;
+    configured.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)l.ctas);
@@ -1285,7 +1360,7 @@ cudaError_t launch_split(const DecodeLaunch& l) {
 }
 
 // One query token per sequence.
-template <int CACHE, bool QBF16>
+template <int CACHE, bool QBF16, int MODE = kModePlain>
 cudaError_t dispatch_split(const DecodeLaunch& l) {
   const int d = l.p.d;
   const int g = l.group;
@@ -1293,8 +1368,8 @@ cudaError_t dispatch_split(const DecodeLaunch& l) {
 #define PKV_CASE(DD, GG)                                                         \
   if (d == DD && g == GG) {                                                      \
     if constexpr (CACHE == kCacheE4M3Tok)                                        \
-      if (deep) return launch_split<DD, GG, 1, CACHE, QBF16, true>(l);           \
-    return launch_split<DD, GG, 1, CACHE, QBF16, false>(l);                      \
+      if (deep) return launch_split<DD, GG, 1, CACHE, QBF16, true, MODE>(l);     \
+    return launch_split<DD, GG, 1, CACHE, QBF16, false, MODE>(l);                \
   }
   if constexpr (!cache_is_fp8((CacheKind)CACHE)) {
     PKV_CASE(64, 1) PKV_CASE(64, 2) PKV_CASE(64, 4) PKV_CASE(64, 8)

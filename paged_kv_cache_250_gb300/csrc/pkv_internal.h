@@ -135,7 +135,20 @@ struct DecodeParams {
   int32_t early_prologue;      // 1: read lengths/tables before waiting on the previous kernel
   int32_t trigger_next;        // 1: let the next kernel on the stream launch at once
   float scale_log2;            // softmax scale * log2(e)
+  // biased scores (MODE kModeBiased): cap log2e (0: no cap), 2 / cap, and one
+  // slope per query head (NULL: no distance bias)
+  float cap_log2, cap_z;
+  const float* slopes;
+  // a shared prefix (MODE kModeShared): its blocks, read through one table for
+  // every sequence (skip_prefix 0) or left to another kernel (1: a sequence's
+  // units start behind them, and lse receives each row's log2 of the weights'
+  // sum, -inf where it has none)
+  const int32_t* prefix_blocks;
+  int32_t npb, skip_prefix;
+  float* lse;                  // [B][Hq]
 };
+// Forms of the single-token kernel.
+constexpr int kModePlain = 0, kModeBiased = 1, kModeShared = 2;
 
 struct DecodeLaunch {
   DecodeParams p;
@@ -204,6 +217,12 @@ inline size_t mq_smem_bytes(int32_t d, CacheKind cache, int32_t B, int32_t nc) {
 
 // Returns a CUDA error (cudaSuccess when the kernel was enqueued) or
 // cudaErrorNotSupported when no kernel is built for the combination.
+cudaError_t launch_decode_biased_f16(const DecodeLaunch& l);
+cudaError_t launch_decode_biased_bf16(const DecodeLaunch& l);
+cudaError_t launch_decode_biased_e4m3(const DecodeLaunch& l);
+cudaError_t launch_decode_biased_e4m3_tok(const DecodeLaunch& l);
+cudaError_t launch_decode_shared_f16(const DecodeLaunch& l);
+cudaError_t launch_decode_shared_bf16(const DecodeLaunch& l);
 cudaError_t launch_decode_f16(const DecodeLaunch& l);
 cudaError_t launch_decode_bf16(const DecodeLaunch& l);
 cudaError_t launch_decode_e4m3(const DecodeLaunch& l);
@@ -232,6 +251,27 @@ cudaError_t decode_workspace_clear(void* workspace, size_t workspace_bytes,
 cudaError_t launch_append(const AppendParams& a, CacheKind cache, bool in_bf16,
                           cudaStream_t stream);
 
+// Append with rotary positions (pkv_rope.cu).
+struct RopeParams {
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slot_mapping;
+  const int64_t* positions;
+  const float* cos_sin;          // [max_position][rot]: rot / 2 cosines, then rot / 2 sines
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;                   // [T][Hq][d]
+  const float* k_scale;
+  const float* v_scale;
+  float* scale_out;              // E4M3 per token: the scale pool (NULL otherwise)
+  int32_t* err_word;
+  int64_t q_stride, k_stride, v_stride;  // elements from token to token
+  int32_t T, Hq, Hkv, d, NB, rot, max_position, interleaved;
+};
+cudaError_t launch_rope_append(const RopeParams& p, CacheKind cache, bool bf16,
+                               cudaStream_t stream);
+
 struct CopyParams {
   void* k_cache;
   void* v_cache;
@@ -257,6 +297,10 @@ struct PrefillParams {
   int32_t B, Hq, Hkv, NB, MBS, total_q, tiles_per_seq;
   pkv_dtype out_dtype;
   float scale_log2;
+  // biased scores only (see DecodeParams); cap_z is 2 log2e scale / cap here
+  float cap_log2, cap_z;
+  const float* slopes;
+  int32_t cap_fine;             // a cap so wide that small scores need the series
 };
 struct PrefillLaunch {
   PrefillParams p;
@@ -267,7 +311,47 @@ struct PrefillLaunch {
   int32_t d;           // head dim: 64 or 128
   cudaStream_t stream;
 };
-size_t prefill_smem_bytes(int d);
+// What is done to the scores before the softmax.
+constexpr int kBiasCap = 1;   // cap tanh(s / cap)
+constexpr int kBiasDist = 2;  // + slope (key position - query position)
+// Caps up to this keep the plain form of the tanh (pkv_device.cuh): its error,
+// 2^-22 of the cap in the score, is at most 2^-16, the weight's own rounding.
+constexpr float kCapCoarse = 64.f;
 cudaError_t launch_prefill(const PrefillLaunch& l);
+cudaError_t launch_prefill_biased(const PrefillLaunch& l);
+
+// Attention over a prefix that a whole batch shares, and its merge with the
+// sequences' own parts (pkv_prefix.cu).
+struct PrefixParams {
+  const int32_t* context_lens;   // [B]
+  const int32_t* prefix_blocks;  // [npb]
+  float* part_o;                 // [Hkv][pairs][2 splits][128 rows][d] unnormalised
+  float* part_ml;                // [Hkv][pairs][2 splits][128 rows] (m in log2 units, l)
+  int32_t* err_word;
+  int32_t B, Hq, Hkv, NB, MBS, npb;
+  int32_t pairs;                 // pairs of 128-row tiles of the B g rows of a KV head
+  int32_t splits;
+  float scale_log2;
+};
+struct PrefixLaunch {
+  PrefixParams p;
+  CUtensorMap tmap_q;  // [B][Hq][d], boxes of 128 / g sequences x g heads x 64
+  CUtensorMap tmap_k;
+  CUtensorMap tmap_v;
+  bool bf16;
+  int32_t d;
+  cudaStream_t stream;
+};
+struct PrefixMergeParams {
+  const float* part_o;
+  const float* part_ml;
+  const float* own_o;            // [B][Hq][d] normalised outputs of the own parts
+  const float* lse;              // [B][Hq] log2 of their weights' sums (-inf: nothing)
+  void* out;
+  int32_t B, Hq, Hkv, pairs, splits;
+  pkv_dtype out_dtype;
+};
+cudaError_t launch_prefix(const PrefixLaunch& l);
+cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int d, cudaStream_t stream);
 
 }  // namespace pkv
