@@ -201,17 +201,51 @@ def _dev_ptr(t: Optional[torch.Tensor], name: str):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _row_ptr(t: torch.Tensor, name: str):
-    """Pointer and token stride of a [tokens][heads][d] tensor whose tokens may
-    lie apart (a part of a fused projection)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens][heads][d]")
-    T, H, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+# The calls below are made every few microseconds by a decode loop: pointers go
+# to ctypes as plain ints, and the current device and stream are read without
+# building torch objects for them.
+def _on(t: Optional[torch.Tensor], dev: int, name: str) -> Optional[int]:
+    """Device address of a contiguous tensor on device dev."""
+    if t is None:
+        return None
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, on the device of q")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_on(t: torch.Tensor, dev: int, name: str, T: int, H: int, d: int):
+    """Device address and token stride of a [T][H][d] tensor on device dev whose
+    tokens may lie apart (a part of a fused projection)."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, on the device of q")
+    if t.shape != (T, H, d):
+        raise ValueError(f"{name} must be [tokens][heads][d], with the cache's heads and d")
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0)) if T > 1 else H * d
+    return t.data_ptr(), st if T > 1 else H * d
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream_on(stream, dev: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _is_current(dev: int) -> bool:
+    """Whether dev is the current device (the library works on that one); a host
+    tensor's -1 passes, to be named by the check of the tensor."""
+    if dev < 0:
+        return True
+    return dev == (_raw_device() if _raw_device is not None else torch.cuda.current_device())
 
 
 def _stream_handle(stream, device) -> ctypes.c_void_p:
@@ -268,29 +302,36 @@ def pkv_kv_append_rope(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Te
     stride; slot_mapping, positions: int64 [T]; cos_sin: fp32
     [max_position][rot_dim], a position's cosines then its sines; q_out:
     [T][Hq][d], which may be q."""
-    lib = load_library()
+    lib = _lib or load_library()
+    dev = q.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_kv_append_rope(desc, k_cache, v_cache, slot_mapping, positions, cos_sin, q,
+                                      k, v, q_out, interleaved, stream)
     if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
         raise ValueError("slot_mapping and positions must be int64")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be fp32 [max_position][rot_dim]")
-    if q.dtype != k.dtype or k.dtype != v.dtype or q_out.dtype != q.dtype:
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt or q_out.dtype != dt:
         raise ValueError("q, k, v and q_out must have one type")
-    if k.shape != v.shape or q_out.shape != q.shape:
-        raise ValueError("k and v, and q and q_out, must have one shape")
-    T = int(k.shape[0])
-    want = ((T, desc.num_q_heads, desc.head_dim), (T, desc.num_kv_heads, desc.head_dim))
-    if tuple(q.shape) != want[0] or tuple(k.shape) != want[1]:
-        raise ValueError("q must be [T][Hq][d], k and v [T][Hkv][d]")
-    if slot_mapping.numel() != T or positions.numel() != T:
+    T, Hq, Hkv, d = slot_mapping.numel(), desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    if positions.numel() != T:
         raise ValueError("slot_mapping and positions need one entry per token")
-    (qp, qs), (kp, ks), (vp, vs) = _row_ptr(q, "q"), _row_ptr(k, "k"), _row_ptr(v, "v")
+    if q_out.shape != (T, Hq, d):
+        raise ValueError("q_out must be [T][Hq][d]")
+    qp, qs = _rows_on(q, dev, "q", T, Hq, d)
+    kp, ks = _rows_on(k, dev, "k", T, Hkv, d)
+    vp, vs = _rows_on(v, dev, "v", T, Hkv, d)
+    max_pos, rot = cos_sin.shape
     st = lib.pkv_kv_append_rope(
-        ctypes.byref(desc), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-        _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(positions, "positions"),
-        _dev_ptr(cos_sin, "cos_sin"), int(cos_sin.shape[0]), int(cos_sin.shape[1]), qp, qs, kp,
-        ks, vp, vs, _dev_ptr(q_out, "q_out"), T, _DTYPE_CODE.get(q.dtype, -1),
-        PKV_ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream, q.device))
-    _check(st, "pkv_kv_append_rope")
+        ctypes.byref(desc), _on(k_cache, dev, "k_cache"), _on(v_cache, dev, "v_cache"),
+        _on(slot_mapping, dev, "slot_mapping"), _on(positions, dev, "positions"),
+        _on(cos_sin, dev, "cos_sin"), max_pos, rot, qp, qs, kp, ks, vp, vs,
+        _on(q_out, dev, "q_out"), T, _DTYPE_CODE.get(dt, -1),
+        PKV_ROPE_INTERLEAVED if interleaved else 0, _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_kv_append_rope")
 
 
 def pkv_copy_blocks(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -393,10 +434,26 @@ def pkv_paged_decode_attention_window(desc: CacheDesc, q: torch.Tensor, k_cache:
     _check(st, "pkv_paged_decode_attention_window")
 
 
-def _check_slopes(alibi_slopes: Optional[torch.Tensor], desc: CacheDesc) -> None:
-    if alibi_slopes is not None:
-        if alibi_slopes.dtype != torch.float32 or alibi_slopes.numel() != desc.num_q_heads:
-            raise ValueError("alibi_slopes must be fp32 with one entry per query head")
+def _bias_on(alibi_slopes: Optional[torch.Tensor], dev: int, desc: CacheDesc) -> Optional[int]:
+    if alibi_slopes is None:
+        return None
+    if alibi_slopes.dtype != torch.float32 or alibi_slopes.numel() != desc.num_q_heads:
+        raise ValueError("alibi_slopes must be fp32 with one entry per query head")
+    return _on(alibi_slopes, dev, "alibi_slopes")
+
+
+def _batch_of(desc: CacheDesc, q: torch.Tensor, out: torch.Tensor, block_tables: torch.Tensor,
+              context_lens: torch.Tensor):
+    """Batch and table width of a single-token call, its shapes checked."""
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    B, mbs = block_tables.shape
+    want = (B, desc.num_q_heads, desc.head_dim)
+    if q.shape != want or out.shape != want:
+        raise ValueError("q and out must be [B][Hq][d]")
+    if context_lens.numel() != B:
+        raise ValueError("context_lens needs one entry per sequence")
+    return B, mbs
 
 
 def pkv_paged_decode_attention_biased(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,
@@ -410,24 +467,23 @@ def pkv_paged_decode_attention_biased(desc: CacheDesc, q: torch.Tensor, k_cache:
     """As pkv_paged_decode_attention, a score s becoming softcap tanh(s /
     softcap) (softcap > 0), then s + alibi_slopes[hq] (u - t) (fp32 [Hq]; key
     position u, query position t); window and sinks as for the windowed call."""
-    lib = load_library()
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise ValueError("block_tables and context_lens must be int32")
-    if q.dim() != 3 or out.shape != q.shape:
-        raise ValueError("q and out must be [B][Hq][d]")
-    _check_slopes(alibi_slopes, desc)
-    B, mbs = int(block_tables.shape[0]), int(block_tables.shape[1])
-    if q.shape[0] != B or context_lens.numel() != B:
-        raise ValueError("q, block_tables and context_lens need one row per sequence")
+    lib = _lib or load_library()
+    dev = q.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_paged_decode_attention_biased(
+                desc, q, k_cache, v_cache, block_tables, context_lens, scale, out, workspace,
+                softcap, alibi_slopes, window, sinks, max_context_len_hint, stream)
+    B, mbs = _batch_of(desc, q, out, block_tables, context_lens)
     st = lib.pkv_paged_decode_attention_biased(
-        ctypes.byref(desc), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables"),
-        _dev_ptr(context_lens, "context_lens"), B, int(window), int(sinks), float(softcap),
-        _dev_ptr(alibi_slopes, "alibi_slopes"), mbs, int(max_context_len_hint), float(scale),
-        _dev_ptr(out, "out"), _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
-        _dev_ptr(workspace, "workspace"), int(workspace.numel() * workspace.element_size()),
-        _stream_handle(stream, q.device))
-    _check(st, "pkv_paged_decode_attention_biased")
+        ctypes.byref(desc), _on(q, dev, "q"), _on(k_cache, dev, "k_cache"),
+        _on(v_cache, dev, "v_cache"), _on(block_tables, dev, "block_tables"),
+        _on(context_lens, dev, "context_lens"), B, int(window), int(sinks), float(softcap),
+        _bias_on(alibi_slopes, dev, desc), mbs, int(max_context_len_hint), float(scale),
+        _on(out, dev, "out"), _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
+        _on(workspace, dev, "workspace"), workspace.nbytes, _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_paged_decode_attention_biased")
 
 
 def pkv_shared_prefix_workspace_bytes(desc: CacheDesc, batch: int, num_prefix_blocks: int,
@@ -452,25 +508,26 @@ def pkv_paged_decode_attention_shared_prefix(desc: CacheDesc, q: torch.Tensor,
     blocks prefix_blocks (int32 [num_prefix_blocks]), which are read once for
     the batch; block_tables holds whole tables, whose entries for the prefix
     are not read, and context_lens whole lengths."""
-    lib = load_library()
-    for t, n in ((prefix_blocks, "prefix_blocks"), (block_tables, "block_tables"),
-                 (context_lens, "context_lens")):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{n} must be int32")
-    if q.dim() != 3 or out.shape != q.shape:
-        raise ValueError("q and out must be [B][Hq][d]")
-    B, mbs = int(block_tables.shape[0]), int(block_tables.shape[1])
-    if q.shape[0] != B or context_lens.numel() != B:
-        raise ValueError("q, block_tables and context_lens need one row per sequence")
+    lib = _lib or load_library()
+    dev = q.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_paged_decode_attention_shared_prefix(
+                desc, q, k_cache, v_cache, prefix_blocks, block_tables, context_lens, scale, out,
+                workspace, max_context_len_hint, stream)
+    if prefix_blocks.dtype != torch.int32:
+        raise ValueError("prefix_blocks must be int32")
+    B, mbs = _batch_of(desc, q, out, block_tables, context_lens)
     st = lib.pkv_paged_decode_attention_shared_prefix(
-        ctypes.byref(desc), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache"), _dev_ptr(prefix_blocks, "prefix_blocks"),
-        int(prefix_blocks.numel()), _dev_ptr(block_tables, "block_tables"),
-        _dev_ptr(context_lens, "context_lens"), B, mbs, int(max_context_len_hint), float(scale),
-        _dev_ptr(out, "out"), _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
-        _dev_ptr(workspace, "workspace"), int(workspace.numel() * workspace.element_size()),
-        _stream_handle(stream, q.device))
-    _check(st, "pkv_paged_decode_attention_shared_prefix")
+        ctypes.byref(desc), _on(q, dev, "q"), _on(k_cache, dev, "k_cache"),
+        _on(v_cache, dev, "v_cache"), _on(prefix_blocks, dev, "prefix_blocks"),
+        prefix_blocks.numel(), _on(block_tables, dev, "block_tables"),
+        _on(context_lens, dev, "context_lens"), B, mbs, int(max_context_len_hint),
+        float(scale),
+        _on(out, dev, "out"), _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
+        _on(workspace, dev, "workspace"), workspace.nbytes, _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_paged_decode_attention_shared_prefix")
 
 
 def pkv_decode_step(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,
@@ -535,26 +592,32 @@ def pkv_paged_prefill_attention_biased(desc: CacheDesc, q: torch.Tensor, k_cache
                                        stream=None) -> None:
     """As pkv_paged_prefill_attention, the scores changed as by
     pkv_paged_decode_attention_biased (t the row's position)."""
-    lib = load_library()
-    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
-                 (q_start, "q_start")):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{n} must be int32")
-    if q.dim() != 3 or out.shape != q.shape:
+    lib = _lib or load_library()
+    dev = q.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_paged_prefill_attention_biased(
+                desc, q, k_cache, v_cache, block_tables, context_lens, q_start, max_q_len, scale,
+                out, softcap, alibi_slopes, stream)
+    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
+            or q_start.dtype != torch.int32):
+        raise ValueError("block_tables, context_lens and q_start must be int32")
+    total = q.shape[0]
+    want = (total, desc.num_q_heads, desc.head_dim)
+    if q.shape != want or out.shape != want:
         raise ValueError("q and out must be [total_q][Hq][d]")
-    _check_slopes(alibi_slopes, desc)
-    B, mbs = int(block_tables.shape[0]), int(block_tables.shape[1])
+    B, mbs = block_tables.shape
     if q_start.numel() != B + 1 or context_lens.numel() != B:
         raise ValueError("q_start needs batch + 1 entries and context_lens batch")
     st = lib.pkv_paged_prefill_attention_biased(
-        ctypes.byref(desc), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables"),
-        _dev_ptr(context_lens, "context_lens"), _dev_ptr(q_start, "q_start"), B,
-        int(q.shape[0]), int(max_q_len), mbs, float(scale), float(softcap),
-        _dev_ptr(alibi_slopes, "alibi_slopes"), _dev_ptr(out, "out"),
-        _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
-        _stream_handle(stream, q.device))
-    _check(st, "pkv_paged_prefill_attention_biased")
+        ctypes.byref(desc), _on(q, dev, "q"), _on(k_cache, dev, "k_cache"),
+        _on(v_cache, dev, "v_cache"), _on(block_tables, dev, "block_tables"),
+        _on(context_lens, dev, "context_lens"), _on(q_start, dev, "q_start"), B, total,
+        int(max_q_len), mbs, float(scale), float(softcap), _bias_on(alibi_slopes, dev, desc),
+        _on(out, dev, "out"),
+        _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1), _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_paged_prefill_attention_biased")
 
 
 def pkv_decode_step_fused(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,

@@ -808,14 +808,16 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const void* k
   l.p.cap_log2 = softcap * 1.4426950408889634f;
   l.p.cap_z = softcap > 0.f ? l.p.scale_log2 * (2.f / softcap) : 0.f;
   l.p.slopes = slopes;
-  l.p.cap_fine = softcap > pkv::kCapCoarse ? 1 : 0;
   if (!(l.p.cap_z < INFINITY)) return PKV_ERR_INVALID_ARG;
   l.bf16 = desc->cache_dtype == PKV_BF16;
   l.d = desc->head_dim;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
   if ((int64_t)batch * l.p.tiles_per_seq >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
-  const cudaError_t e = softcap > 0.f || slopes != nullptr ? pkv::launch_prefill_biased(l)
-                                                           : pkv::launch_prefill(l);
+  const bool fine = softcap > pkv::kCapCoarse;
+  const cudaError_t e = fine              ? pkv::launch_prefill_cap_fine(l)
+                        : softcap > 0.f   ? pkv::launch_prefill_cap(l)
+                        : slopes != nullptr ? pkv::launch_prefill_dist(l)
+                                            : pkv::launch_prefill(l);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 }  // namespace

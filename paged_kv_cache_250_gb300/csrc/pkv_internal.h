@@ -300,7 +300,6 @@ struct PrefillParams {
   // biased scores only (see DecodeParams); cap_z is 2 log2e scale / cap here
   float cap_log2, cap_z;
   const float* slopes;
-  int32_t cap_fine;             // a cap so wide that small scores need the series
 };
 struct PrefillLaunch {
   PrefillParams p;
@@ -314,11 +313,14 @@ struct PrefillLaunch {
 // What is done to the scores before the softmax.
 constexpr int kBiasCap = 1;   // cap tanh(s / cap)
 constexpr int kBiasDist = 2;  // + slope (key position - query position)
+constexpr int kBiasFine = 4;  // with kBiasCap: small scores under a wide cap keep every bit
 // Caps up to this keep the plain form of the tanh (pkv_device.cuh): its error,
 // 2^-22 of the cap in the score, is at most 2^-16, the weight's own rounding.
 constexpr float kCapCoarse = 64.f;
 cudaError_t launch_prefill(const PrefillLaunch& l);
-cudaError_t launch_prefill_biased(const PrefillLaunch& l);
+cudaError_t launch_prefill_cap(const PrefillLaunch& l);       // with or without slopes
+cudaError_t launch_prefill_cap_fine(const PrefillLaunch& l);  // with or without slopes
+cudaError_t launch_prefill_dist(const PrefillLaunch& l);
 
 // Attention over a prefix that a whole batch shares, and its merge with the
 // sequences' own parts (pkv_prefix.cu).

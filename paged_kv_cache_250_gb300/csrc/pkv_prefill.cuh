@@ -79,7 +79,12 @@ struct Masked {
 };
 
 // BIAS: what is done to the scores before the softmax: kBiasCap caps them by a
-// tanh, kBiasDist adds a bias that grows with the distance (0: neither).
+// tanh, kBiasDist adds a bias that grows with the distance (0: neither);
+// kBiasFine beside kBiasCap for caps above kCapCoarse.  A cap alone keeps the
+// order of the scores, so the max pass takes raw scores and caps their maximum;
+// with both, the max pass writes what the P pass needs back over the scores, so
+// that the tanh (four of the six special-function results of a pair) is
+// computed once.
 template <bool BF16, int D, int BIAS>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmq,
@@ -301,17 +306,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     auto dist_of = [&](int t0) -> uint64_t {
       return f2(slope2 * (float)(t0 - vis), slope2 * (float)(t0 + 1 - vis));
     };
-    // two raw scores capped (log2 units)
-    auto cap_pair = [&](uint64_t raw) -> uint64_t {
-      const uint64_t z2 = mul2(raw, cz2);
-      const float2 z = f2_split(z2);
+    // two raw scores capped (log2 units), plus `add`
+    constexpr bool kFine = (BIAS & kBiasFine) != 0;
+    auto cap_pair = [&](uint64_t raw, uint64_t add) -> uint64_t {
+      const float2 z = f2_split(mul2(raw, cz2));
       const float2 u = f2_split(add2(f2(ex2(z.x), ex2(z.y)), f2(1.f, 1.f)));
-      uint64_t r = fma2(f2(rcp(u.x), rcp(u.y)), mcap2, cap2);
-      if (p.cap_fine) {  // a wide cap: near 0 by the series, which keeps every bit
-        const float2 f = f2_split(r);
-        r = f2(cap_near_zero(z.x, p.cap_log2, f.x), cap_near_zero(z.y, p.cap_log2, f.y));
-      }
-      return r;
+      const uint64_t r = f2(rcp(u.x), rcp(u.y));
+      if constexpr (!kFine) return fma2(r, mcap2, add2(cap2, add));
+      // a wide cap: near 0 by the series, which keeps every bit
+      const float2 f = f2_split(fma2(r, mcap2, cap2));
+      return add2(f2(cap_near_zero(z.x, p.cap_log2, f.x), cap_near_zero(z.y, p.cap_log2, f.y)),
+                  add);
     };
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // row max of the raw scores (c2 > 0 commutes with the max): quarters
       // 3, 2, 1, 0, so quarter 0 is still in sb when the P pass starts
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto qmax = [&](auto mc, const uint32_t (&sq)[32], int qq) {
+      auto qmax = [&](auto mc, uint32_t (&sq)[32], int qq) {
         if constexpr (kDist) {  // of the biased scores
           const int t0 = tok0 + 32 * qq;
           uint64_t db = dist_of(t0);
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           for (int i = 0; i < 16; ++i) {
             const uint64_t raw = f2(__uint_as_float(sq[2 * i]), __uint_as_float(sq[2 * i + 1]));
             float2 y;
-            if constexpr (kCap) y = f2_split(add2(cap_pair(raw), db));
+            if constexpr (kCap) y = f2_split(cap_pair(raw, db));
             else y = f2_split(fma2(raw, f2(c2, c2), db));
             db = add2(db, dist_step);
             if constexpr (decltype(mc)::value) {
@@ -345,6 +350,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               if (t0 + 2 * i + 1 > vis) y.y = -INFINITY;
             }
             m4[i & 3] = max3(m4[i & 3], y.x, y.y);
+            if constexpr (kCap) {
+              sq[2 * i] = __float_as_uint(y.x);
+              sq[2 * i + 1] = __float_as_uint(y.y);
+            }
+          }
+          if constexpr (kCap) {  // quarter 0 stays in registers
+            if (qq > 0) tmem_st32_issue(t_s + 32 * qq, sq);
           }
         } else if constexpr (!decltype(mc)::value) {
 #pragma unroll
@@ -373,13 +385,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         qmax(mc, sa, 1);
         tmem_ld_wait(sb);
         qmax(mc, sb, 0);
+        if constexpr (kCap && kDist) tmem_st_wait();
       };
       if (full) max_pass(Masked<false>{});
       else max_pass(Masked<true>{});
       float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       if constexpr (!kDist) {  // the cap keeps the order of the scores: the largest alone
         if constexpr (kCap) {
-          if (mx > -INFINITY) mx = f2_split(cap_pair(f2(mx, mx))).x;
+          if (mx > -INFINITY) mx = f2_split(cap_pair(f2(mx, mx), f2(0.f, 0.f))).x;
         } else {
           mx *= c2;
         }
@@ -418,14 +431,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       uint32_t hi[16], lo[16];
       auto qp = [&](auto mc, const uint32_t (&sq)[32], int qq) {
         uint64_t sub = nmu2;  // minus the reference, plus the distance bias
-        if constexpr (kDist) sub = add2(dist_of(tok0 + 32 * qq), nmu2);
+        if constexpr (kDist && !kCap) sub = add2(dist_of(tok0 + 32 * qq), nmu2);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const uint64_t raw = f2(__uint_as_float(sq[2 * i]), __uint_as_float(sq[2 * i + 1]));
           float2 y;
-          if constexpr (kCap) y = f2_split(add2(cap_pair(raw), sub));
+          if constexpr (kCap && kDist) y = f2_split(add2(raw, sub));  // capped and biased before
+          else if constexpr (kCap) y = f2_split(cap_pair(raw, sub));
           else y = f2_split(fma2(raw, c2x2, sub));
-          if constexpr (kDist) sub = add2(sub, dist_step);
+          if constexpr (kDist && !kCap) sub = add2(sub, dist_step);
           float p0 = ex2(y.x), p1 = ex2(y.y);
           if constexpr (decltype(mc)::value) {
             const int tk = tok0 + 32 * qq + 2 * i;
