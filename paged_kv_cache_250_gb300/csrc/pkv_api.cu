@@ -205,50 +205,27 @@ pkv_status bias_checks(float softcap, const float* slopes) {
 }
 
 // Shared prefix: the front of the workspace.  Sizes grow with the batch alone
-// (the partials of at most kPrefixItems CTAs, or of one per pair of row tiles
-// when there are more pairs), so a workspace for a batch serves smaller ones.
+// (the prefix's partials: one slot per CTA and segment; the own parts': one per
+// chunk), so a workspace for a batch serves smaller ones.
+constexpr int64_t kOwnItems = 4096;  // chunks of own parts over the batch, about
+constexpr int32_t kOwnPages = 8;     // pages of a chunk, at least
 struct SharedLayout {
-  size_t lse_off, own_off, ml_off, o_off, total;
+  size_t pre_ml, pre_o, own_ml, own_o, total;
   int32_t pairs;
 };
-constexpr int64_t kPrefixItemsPerSm = 2;
 SharedLayout shared_layout(const pkv_cache_desc* d, int32_t batch, int sms) {
-  const int64_t rows = (int64_t)batch * (d->num_q_heads / d->num_kv_heads);
+  const int64_t g = d->num_q_heads / d->num_kv_heads;
+  const int64_t segs = (int64_t)batch * d->num_kv_heads;
   SharedLayout s;
-  s.pairs = (int32_t)((rows + 255) / 256);
-  const int64_t least = (int64_t)s.pairs * d->num_kv_heads;
-  const int64_t items = least > kPrefixItemsPerSm * sms ? least : kPrefixItemsPerSm * sms;
-  const int64_t outs = (int64_t)batch * d->num_q_heads;
-  s.lse_off = 0;
-  s.own_off = align256(outs * sizeof(float));
-  s.ml_off = align256(s.own_off + outs * d->head_dim * sizeof(float));
-  s.o_off = align256(s.ml_off + items * 256 * 2 * sizeof(float));
-  s.total = align256(s.o_off + items * 256 * d->head_dim * sizeof(float));
+  s.pairs = (int32_t)(((int64_t)batch * g + 255) / 256);
+  const int64_t pre_rows = ((int64_t)sms + (int64_t)s.pairs * d->num_kv_heads) * 256;
+  const int64_t own_rows = (segs > kOwnItems ? segs : kOwnItems) * g;
+  s.pre_ml = 256;
+  s.pre_o = align256(s.pre_ml + pre_rows * 2 * sizeof(float));
+  s.own_ml = align256(s.pre_o + pre_rows * d->head_dim * sizeof(float));
+  s.own_o = align256(s.own_ml + own_rows * 2 * sizeof(float));
+  s.total = align256(s.own_o + own_rows * d->head_dim * sizeof(float));
   return s;
-}
-
-// CTAs the blocks of a pair of row tiles are cut over: the count that makes
-// the longest SM's work least, at kBlockCost per block (of 128 tokens) a CTA
-// takes and kCtaCost for its start and end.
-int32_t shared_splits(const pkv_cache_desc* d, int32_t batch, int32_t npb, const SharedLayout& s,
-                      int sms) {
-  constexpr int64_t kBlockCost = 2, kCtaCost = 5;
-  const int64_t least = (int64_t)s.pairs * d->num_kv_heads;
-  const int64_t nblk = ((int64_t)npb * kPageSize + 127) / 128;
-  int64_t most = kPrefixItemsPerSm * sms / least;
-  if (most > nblk) most = nblk;
-  (void)batch;
-  int32_t best = 1;
-  int64_t best_cost = -1;
-  for (int64_t n = 1; n <= most; ++n) {
-    const int64_t waves = (least * n + sms - 1) / sms;
-    const int64_t cost = waves * (kBlockCost * ((nblk + n - 1) / n) + kCtaCost);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = (int32_t)n;
-    }
-  }
-  return best;
 }
 
 // Whether the prefix is worth a pass of its own; otherwise every sequence reads
@@ -334,8 +311,6 @@ struct DecodeForm {
   const float* slopes = nullptr;
   const int32_t* prefix_blocks = nullptr;
   int32_t npb = 0;
-  int32_t skip_prefix = 0;
-  float* lse = nullptr;
 };
 
 pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_cache,
@@ -352,15 +327,8 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
                                 out_dtype, workspace, workspace_bytes, qlen);
   if (st != PKV_OK || batch == 0) return st;
   const int sms = sm_count_current_device();
-  WsLayout w =
+  const WsLayout w =
       ws_layout(desc, batch, max_blocks_per_seq, max_context_len_hint, sms, nc_of(desc, qlen));
-  if (form.skip_prefix) {  // fewer units; the layout is the same
-    const int32_t skip = form.npb * kPageSize;
-    const int32_t hint = max_context_len_hint > skip ? max_context_len_hint - skip : 0;
-    w.ctas = ws_layout(desc, batch, max_blocks_per_seq - form.npb,
-                       max_context_len_hint > 0 && hint == 0 ? 1 : hint, sms,
-                       nc_of(desc, qlen)).ctas;
-  }
   pkv::DecodeLaunch l;
   st = encode_cache_map(&l.tmap_k, k_cache, desc);
   if (st != PKV_OK) return st;
@@ -400,8 +368,6 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
   l.p.slopes = form.slopes;
   l.p.prefix_blocks = form.prefix_blocks;
   l.p.npb = form.npb;
-  l.p.skip_prefix = form.skip_prefix;
-  l.p.lse = form.lse;
   l.group = desc->num_q_heads / desc->num_kv_heads;
   // query-token capacity of the kernel: 1, or the smallest of 2, 4, 8 that
   // holds qlen
@@ -705,7 +671,7 @@ pkv_status pkv_paged_decode_attention_shared_prefix(
                        max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype, out_dtype,
                        own, own_bytes, stream, /*early_prologue=*/0, 1, 0, 0, nullptr, nullptr,
                        PKV_BF16, 0, form);
-  // the prefix for all rows at once, then each sequence's own part, then the merge
+  // the prefix for all rows at once, each sequence's own part, the merge
   pkv::PrefixLaunch l;
   st = encode_cache_map(&l.tmap_k, k_cache, desc);
   if (st != PKV_OK) return st;
@@ -713,10 +679,16 @@ pkv_status pkv_paged_decode_attention_shared_prefix(
   if (st != PKV_OK) return st;
   st = encode_q_map(&l.tmap_q, q, desc, batch);
   if (st != PKV_OK) return st;
+  l.p.q = q;
   l.p.context_lens = context_lens;
   l.p.prefix_blocks = prefix_blocks;
-  l.p.part_ml = reinterpret_cast<float*>(ws + s.ml_off);
-  l.p.part_o = reinterpret_cast<float*>(ws + s.o_off);
+  l.p.block_tables = block_tables;
+  l.p.out = out;
+  l.p.seen = reinterpret_cast<int32_t*>(ws);
+  l.p.pre_ml = reinterpret_cast<float2*>(ws + s.pre_ml);
+  l.p.pre_o = reinterpret_cast<float*>(ws + s.pre_o);
+  l.p.own_ml = reinterpret_cast<float2*>(ws + s.own_ml);
+  l.p.own_o = reinterpret_cast<float*>(ws + s.own_o);
   l.p.err_word = desc->err_word;
   l.p.B = batch;
   l.p.Hq = desc->num_q_heads;
@@ -725,34 +697,28 @@ pkv_status pkv_paged_decode_attention_shared_prefix(
   l.p.MBS = max_blocks_per_seq;
   l.p.npb = num_prefix_blocks;
   l.p.pairs = s.pairs;
-  l.p.splits = shared_splits(desc, batch, num_prefix_blocks, s, sms);
+  l.p.ctas = sms;
+  // own parts are cut into chunks of kOwnPages pages or more, about kOwnItems in
+  // all (from the longest own part the arguments allow: empty chunks are cheap)
+  const int64_t cap = (int64_t)max_blocks_per_seq * kPageSize;
+  const int64_t longest =
+      max_context_len_hint > 0 && max_context_len_hint < cap ? max_context_len_hint : cap;
+  int64_t most_own = (longest + kPageSize - 1) / kPageSize - num_prefix_blocks;
+  if (most_own < 1) most_own = 1;
+  const int64_t segs = (int64_t)batch * desc->num_kv_heads;
+  int64_t chunks = kOwnItems / segs;
+  if (chunks > (most_own + kOwnPages - 1) / kOwnPages)
+    chunks = (most_own + kOwnPages - 1) / kOwnPages;
+  if (chunks < 1) chunks = 1;
+  l.p.chunks = (int32_t)chunks;
+  l.p.chunk_pages = (int32_t)((most_own + chunks - 1) / chunks);
+  l.p.out_dtype = out_dtype;
   l.p.scale_log2 = scale * 1.4426950408889634f;
   l.bf16 = desc->cache_dtype == PKV_BF16;
   l.d = desc->head_dim;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
-  if (pkv::launch_prefix(l) != cudaSuccess) return PKV_ERR_CUDA;
-  form.skip_prefix = 1;
-  form.lse = reinterpret_cast<float*>(ws + s.lse_off);
-  float* own_o = reinterpret_cast<float*>(ws + s.own_off);
-  st = decode_impl(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
-                   max_blocks_per_seq, max_context_len_hint, scale, own_o, q_dtype, PKV_F32, own,
-                   own_bytes, stream, /*early_prologue=*/0, 1, 0, 0, nullptr, nullptr, PKV_BF16,
-                   0, form);
-  if (st != PKV_OK) return st;
-  pkv::PrefixMergeParams m;
-  m.part_o = l.p.part_o;
-  m.part_ml = l.p.part_ml;
-  m.own_o = own_o;
-  m.lse = form.lse;
-  m.out = out;
-  m.B = batch;
-  m.Hq = desc->num_q_heads;
-  m.Hkv = desc->num_kv_heads;
-  m.pairs = s.pairs;
-  m.splits = l.p.splits;
-  m.out_dtype = out_dtype;
-  return pkv::launch_prefix_merge(m, desc->head_dim, l.stream) == cudaSuccess ? PKV_OK
-                                                                              : PKV_ERR_CUDA;
+  if (segs * chunks >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
+  return pkv::launch_prefix(l) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -145,7 +145,7 @@ __device__ __forceinline__ void store_out_rt(pkv_dtype t, void* base, int64_t id
 // MODE: kModeBiased caps the scores by a tanh and / or adds a bias that grows
 // with the distance, a handful of instructions on the four scores a lane holds
 // of a page; kModeShared reads a prefix that all sequences share through its
-// own table, or leaves it out and writes each row's log2 sum for the merge.
+// own table.
 template <int D, int G, int QC, int CACHE, bool QBF16, bool DEEP, int MODE>
 __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCtasPerSm)
     decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
-  if (!p.early_prologue && !(kShared && p.skip_prefix)) griddep_wait();
+  if (!p.early_prologue) griddep_wait();
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -236,17 +236,11 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
         sk = fw - nsp;
       }
     }
-    if constexpr (kShared) {  // the prefix is a gap before the sequence's first unit
-      if (p.skip_prefix) {
-        ns = 0;
-        sk = min(np, p.npb);
-      }
-    }
     ctxs[b] = c;
     gns[b] = ns;
     gsk[b] = sk;
     pfx[b + 1] = np - sk;
-    nzp[b + 1] = np - (kShared ? sk : 0) > 0 ? 1 : 0;
+    nzp[b + 1] = np > 0 ? 1 : 0;
   }
   if (lane == 0) {
     for (int s = 0; s < kS; ++s) mbar_init(smem_u32(&bars[warp * kS + s]), 1);
@@ -503,10 +497,6 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     const int64_t row0 = (int64_t)b * p.qlen * p.Hq * D;
     for (int i = tid; i < p.qlen * p.Hq * D; i += blockDim.x)
       store_out_rt(p.out_dtype, p.out, row0 + i, 0.f);
-    if constexpr (kShared) {
-      if (p.skip_prefix)
-        for (int i = tid; i < p.Hq; i += blockDim.x) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
-    }
   }
 
   // ---- per-lane fragment coordinates
@@ -971,10 +961,6 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
           }
         }
       }
-      if constexpr (kShared) {
-        if (p.skip_prefix && col % (D / 4) == 0)
-          p.lse[col_row(b, h, head)] = lsum != 0.f ? M + log2f(lsum) : -INFINITY;
-      }
       const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
       const int64_t ob = col_row(b, h, head) * D + (col % (D / 4)) * 4;
       store_out_rt(p.out_dtype, p.out, ob + 0, acc.x * inv);
@@ -1070,12 +1056,6 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       const float i0 = lt0 > 0.f ? vs / lt0 : 0.f;
       const float i1 = lt1 > 0.f ? vs / lt1 : 0.f;
       const bool w0 = col_real(h0), w1 = col_real(h1);
-      if constexpr (kShared) {
-        if (p.skip_prefix && r8 == 0) {
-          if (w0) p.lse[col_row(b, h, h0)] = lt0 != 0.f ? m2[0] + log2f(lt0) : -INFINITY;
-          if (w1) p.lse[col_row(b, h, h1)] = lt1 != 0.f ? m2[1] + log2f(lt1) : -INFINITY;
-        }
-      }
       const int64_t ob0 = (w0 ? col_row(b, h, h0) : 0) * D;
       const int64_t ob1 = (w1 ? col_row(b, h, h1) : 0) * D;
 #pragma unroll
@@ -1320,11 +1300,6 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     for (int q = k_dead; q < issued; ++q)
       mbar_wait_bounded(smem_u32(&bars[warp * kS + (q % kS)]), (uint32_t)((q / kS) & 1),
                         kWaitLimitNs);
-  }
-  if constexpr (kShared) {
-    // this pass read nothing of the prefix kernel before it on the stream; the
-    // merge behind it waits for this kernel alone, so this one ends after both
-    if (p.skip_prefix) griddep_wait();
   }
 }
 

@@ -139,13 +139,10 @@ struct DecodeParams {
   // slope per query head (NULL: no distance bias)
   float cap_log2, cap_z;
   const float* slopes;
-  // a shared prefix (MODE kModeShared): its blocks, read through one table for
-  // every sequence (skip_prefix 0) or left to another kernel (1: a sequence's
-  // units start behind them, and lse receives each row's log2 of the weights'
-  // sum, -inf where it has none)
+  // a shared prefix (MODE kModeShared): the blocks of every sequence's first
+  // npb pages
   const int32_t* prefix_blocks;
-  int32_t npb, skip_prefix;
-  float* lse;                  // [B][Hq]
+  int32_t npb;
 };
 // Forms of the single-token kernel.
 constexpr int kModePlain = 0, kModeBiased = 1, kModeShared = 2;
@@ -322,17 +319,28 @@ cudaError_t launch_prefill_cap(const PrefillLaunch& l);       // with or without
 cudaError_t launch_prefill_cap_fine(const PrefillLaunch& l);  // with or without slopes
 cudaError_t launch_prefill_dist(const PrefillLaunch& l);
 
-// Attention over a prefix that a whole batch shares, and its merge with the
-// sequences' own parts (pkv_prefix.cu).
+// Attention over a prefix that a whole batch shares, over the sequences' own
+// parts, and their merge (pkv_prefix.cu).
 struct PrefixParams {
+  const void* q;                 // [B][Hq][d]
   const int32_t* context_lens;   // [B]
   const int32_t* prefix_blocks;  // [npb]
-  float* part_o;                 // [Hkv][pairs][2 splits][128 rows][d] unnormalised
-  float* part_ml;                // [Hkv][pairs][2 splits][128 rows] (m in log2 units, l)
+  const int32_t* block_tables;   // [B][MBS]
+  void* out;                     // [B][Hq][d]
+  int32_t* seen;                 // longest stretch of the prefix any sequence sees
+  // Partials: the prefix kernel's CTA c leaves its part of segment s (pair of
+  // row tiles x KV head) in slot c + s: [slot][2 streams][128 rows].  A chunk
+  // of a sequence's own part is slot (b Hkv + h) chunks + chunk: [slot][g].
+  float2* pre_ml;                // (m in log2 units, l)
+  float* pre_o;                  // [d] each, unnormalised
+  float2* own_ml;
+  float* own_o;
   int32_t* err_word;
   int32_t B, Hq, Hkv, NB, MBS, npb;
   int32_t pairs;                 // pairs of 128-row tiles of the B g rows of a KV head
-  int32_t splits;
+  int32_t ctas;                  // of the prefix kernel, at most
+  int32_t chunks, chunk_pages;   // of an own part
+  pkv_dtype out_dtype;
   float scale_log2;
 };
 struct PrefixLaunch {
@@ -344,16 +352,13 @@ struct PrefixLaunch {
   int32_t d;
   cudaStream_t stream;
 };
-struct PrefixMergeParams {
-  const float* part_o;
-  const float* part_ml;
-  const float* own_o;            // [B][Hq][d] normalised outputs of the own parts
-  const float* lse;              // [B][Hq] log2 of their weights' sums (-inf: nothing)
-  void* out;
-  int32_t B, Hq, Hkv, pairs, splits;
-  pkv_dtype out_dtype;
-};
-cudaError_t launch_prefix(const PrefixLaunch& l);
-cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int d, cudaStream_t stream);
+// CTAs of the prefix kernel with work: a share is at least two blocks of 128
+// tokens of a pair of row tiles (a block costs 2, or 1 where the second tile
+// is empty).
+__host__ __device__ inline int64_t prefix_ctas(int64_t cost, int32_t ctas) {
+  const int64_t most = cost / 4 > 0 ? cost / 4 : 1;
+  return most < ctas ? most : ctas;
+}
+cudaError_t launch_prefix(const PrefixLaunch& l);  // the three kernels
 
 }  // namespace pkv

@@ -1,28 +1,39 @@
-// Attention of a whole batch over a prefix that its sequences share, on the
-// 5th-generation tensor cores, and the merge with the sequences' own parts.
+// Decode attention of a batch whose sequences share a prefix: the prefix for
+// the whole batch on the 5th-generation tensor cores, the sequences' own parts,
+// and the merge.
 //
 // Every (sequence, query head) row of one KV head multiplies the same K and V
-// blocks, so the prefix is a dense product of R = B g rows (g query heads per
-// KV head) with 128-token blocks, each block read once per 256 rows instead
-// of once per sequence.  Per row the kernel keeps the running maximum m and
-// sum l of an online softmax and the unnormalised output o; the blocks are
-// cut over S CTAs, each leaving its (m, l, o) as a partial, and
+// blocks of the prefix, so it is a dense product of R = B g rows (g query heads
+// per KV head) with 128-token blocks, each block read once per 256 rows instead
+// of once per sequence.  Per row every part keeps the running maximum m and sum
+// l of an online softmax and the unnormalised output o, and
 //   out = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M),   M = max_i m_i,
-// over the prefix's partials and the row's own part (normalised, with its log2
-// sum in the place of m and l = 1).
+// over the parts of the prefix and of the row's own tokens.
 //
-// One CTA per (pair of 128-row tiles, KV head, split), with fixed roles that
-// hand over through mbarriers, as the prefill kernel's:
+// prefix_kernel.  The (pair of 128-row tiles, KV head, block) units lie on one
+// line, cut into equal shares, one per CTA of at most one CTA per SM; a share
+// crosses a few segments (pair, KV head) and leaves one partial in each.  Roles
+// hand over through mbarriers, as in the prefill kernel:
 //   warps 0-3, 4-7  softmax of stream 0, 1: one row per thread, TMEM lane t;
 //   warp 8          issues the MMAs; warp 9 the tensor copies.
 // A stream is a row tile with its accumulator.  Two tiles of rows share every
-// block (K and V double-buffered); with one tile left, both streams are that
-// tile, stream t taking every second block in buffer t, so the tensor cores
-// still work on one stream under the other's softmax.
+// block (K and V double-buffered); where the second tile of a pair is empty,
+// both streams are the first tile, stream t taking every second block in
+// buffer t, so the tensor cores still work on one stream under the other's
+// softmax.
 //   S = Q K^T   tcgen05.mma M 128 x N 128 x K d from shared memory;
 //   P           hi + lo 16-bit pairs over S in tensor memory (the weights keep
 //               about 16 bits, as in the framework's other attention kernels);
 //   O += P V    tcgen05.mma with A from tensor memory, twice per 16 tokens.
+//
+// own_kernel.  One warp per CTA and per chunk of one sequence's own pages of
+// one KV head: the page ring, MMAs and softmax of the single-token decode
+// kernel's warp, with nothing to hand over at a segment's end.  It depends on
+// nothing the prefix kernel writes and needs little of an SM (a 24 KB ring), so
+// it is launched to run beside it: the prefix is bound by the tensor cores and
+// its softmax, the own parts by HBM.
+//
+// prefix_merge_kernel.  A warp per row adds the parts in a fixed order.
 #include <atomic>
 
 #include "pkv_device.cuh"
@@ -47,13 +58,68 @@ struct Plan {
   static constexpr uint32_t kOffK = 2 * NH * kHalf;
   static constexpr uint32_t kOffV = 4 * NH * kHalf;
   static constexpr uint32_t kOffBar = 6 * NH * kHalf;
-  static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort, counts, max
+  static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort, max, counts
   static constexpr size_t kSmem = 1024 + kOffMisc + 12 + 4 * kNumBars;
 };
 template <bool B>
 struct Masked {
   static constexpr bool value = B;
 };
+
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+constexpr int64_t kMergeRows = 1024;
+
+// tokens of the prefix that a sequence of length c sees (bad lengths: none; the
+// own kernel reports them)
+__device__ __forceinline__ int prefix_len(int c, const PrefixParams& p) {
+  return c < 0 || c > p.MBS * kPageSize ? 0 : min(c, p.npb * kPageSize);
+}
+
+// The line of units: pair-major, then KV head, then block.  A block of a pair
+// costs w = 2, or 1 where the second tile is empty (only in the last pair).
+struct Line {
+  int Hkv, pairs, nblk, last_w;
+  int64_t cost, n;  // whole cost; CTAs with work
+  __device__ Line(const PrefixParams& p, int seen)
+      : Hkv(p.Hkv), pairs(p.pairs), nblk((seen + kTok - 1) / kTok) {
+    last_w = (2 * pairs - 1) * kRows < p.B * (p.Hq / p.Hkv) ? 2 : 1;
+    cost = (int64_t)Hkv * nblk * (2 * (pairs - 1) + last_w);
+    n = prefix_ctas(cost, p.ctas);
+  }
+  __device__ int weight(int pair) const { return pair == pairs - 1 ? last_w : 2; }
+  __device__ int64_t start(int pair, int h) const {
+    return (int64_t)Hkv * nblk * 2 * pair + (int64_t)h * nblk * weight(pair);
+  }
+  __device__ int64_t share(int64_t c) const { return (c * cost + n - 1) / n; }  // first cost of CTA c
+  __device__ int64_t cta_of(int64_t x) const { return x * n / cost; }
+};
+// One CTA's blocks of one segment.
+struct Part {
+  int pair, h, j0, nblk;
+  bool two;
+};
+// Steps through the segments that the costs [x, hi) cross; false at the end.
+// A unit belongs to the share its first cost lies in.
+__device__ __forceinline__ bool next_part(const Line& ln, int64_t& x, int64_t hi, Part& s) {
+  while (x < hi) {
+    const int64_t per = (int64_t)ln.Hkv * ln.nblk * 2;
+    s.pair = (int)min(x / per, (int64_t)(ln.pairs - 1));
+    const int w = ln.weight(s.pair);
+    s.two = w == 2;
+    const int64_t seg = (int64_t)ln.nblk * w;
+    s.h = (int)((x - per * s.pair) / seg);
+    const int64_t s0 = ln.start(s.pair, s.h);
+    s.j0 = (int)((x - s0 + w - 1) / w);
+    const int64_t j1 = min((int64_t)ln.nblk, (hi - s0 + w - 1) / w);
+    s.nblk = (int)(j1 - s.j0);
+    x = s0 + seg;
+    if (s.nblk > 0) return true;
+  }
+  return false;
+}
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -64,11 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NH = PL::NH;
   constexpr uint32_t kOffK = PL::kOffK, kOffV = PL::kOffV, kOffBar = PL::kOffBar,
                      kOffMisc = PL::kOffMisc;
-  const int pair = blockIdx.x % p.pairs, split = blockIdx.x / p.pairs;
-  const int h = blockIdx.y;
   const int G = p.Hq / p.Hkv;
-  const int R = p.B * G;
-  const bool two = (2 * pair + 1) * kRows < R;  // two tiles of rows, else two streams of one
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -106,26 +168,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the positions any sequence sees of the prefix: rows of V behind them may
   // never have been written
-  auto ctx_of = [&](int b) -> int {  // what a sequence sees; the suffix pass reports bad lengths
-    const int c = p.context_lens[b];
-    return c < 0 || c > p.MBS * kPageSize ? 0 : min(c, p.npb * kPageSize);
-  };
   {
     int m = 0;
-    for (int b = tid; b < p.B; b += kThreads) m = max(m, ctx_of(b));
+    for (int b = tid; b < p.B; b += kThreads) m = max(m, prefix_len(p.context_lens[b], p));
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0 && m > 0) atomicMax(max_len, m);
   }
   __syncthreads();
   const int seen = *max_len;
-  const int nblk_all = (seen + kTok - 1) / kTok;
-  const int blk0 = (int)((int64_t)nblk_all * split / p.splits);
-  const int nblk = (int)((int64_t)nblk_all * (split + 1) / p.splits) - blk0;
-  // stream t's blocks: blk0 + i (two tiles) or blk0 + 2 i + t (one)
-  auto count_of = [&](int t) -> int { return two ? nblk : (nblk + 1 - t) / 2; };
-  auto block_of = [&](int t, int i) -> int { return blk0 + (two ? i : 2 * i + t); };
-  auto buf_of = [&](int t, int i) -> int { return two ? i & 1 : t; };
-  auto use_of = [&](int i) -> int { return two ? i >> 1 : i; };  // of the buffer
+  if (blockIdx.x == 0 && tid == 0) *p.seen = seen;  // for the merge
+  const Line line(p, seen);
+  const int64_t lo = blockIdx.x < line.n && seen > 0 ? line.share(blockIdx.x) : 0;
+  const int64_t hi = blockIdx.x < line.n && seen > 0 ? line.share(blockIdx.x + 1) : 0;
+
+  // Every role steps through the same parts.  Stream t's i-th block of a part is
+  // j0 + i (two tiles) or j0 + 2 i + t (one), in buffer i & 1 or t; use counts
+  // of the buffers and the streams run on from part to part (they give the
+  // barriers' phases).
+  struct Walk {
+    Part s;
+    int buf0 = 0, buf1 = 0, str0 = 0, str1 = 0;  // uses before this part
+    __device__ int count(int t) const { return s.two ? s.nblk : (s.nblk + 1 - t) / 2; }
+    __device__ int block(int t, int i) const { return s.j0 + (s.two ? i : 2 * i + t); }
+    __device__ int buf(int t, int i) const { return s.two ? i & 1 : t; }
+    __device__ int use(int t, int i) const {
+      return (buf(t, i) ? buf1 : buf0) + (s.two ? i >> 1 : i);
+    }
+    __device__ int str(int t) const { return t ? str1 : str0; }
+    __device__ void done() {
+      buf0 += (s.nblk + 1) / 2;
+      buf1 += s.nblk / 2;
+      str0 += count(0);
+      str1 += count(1);
+    }
+  } wk;
+  int64_t at = lo;
 
   auto wait = [&](int i, uint32_t parity) -> bool {
     if (*abort_flag) return false;
@@ -136,31 +213,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 9) {
     // ------------------------------------------------------------ copies
-    if (nblk > 0) {
+    bool ok = true;
+    while (ok && next_part(line, at, hi, wk.s)) {
+      // Q's tiles are free when every product of the last part with them is done
+      for (int bb = 0; ok && bb < 2; ++bb) {
+        const int u = bb ? wk.buf1 : wk.buf0;
+        if (u > 0)
+          ok = __all_sync(0xffffffffu, wait(kBarKFree + bb, (uint32_t)((u - 1) & 1)));
+      }
+      if (!ok) break;
       if (lane == 0) {
-        armed[kBarQ] = 1;
-        const int nq = two ? 2 : 1;
+        armed[kBarQ] = armed[kBarQ] + 1;
+        const int nq = wk.s.two ? 2 : 1;
         mbar_arrive_expect_tx(bar(kBarQ), (uint32_t)nq * NH * kHalf);
         for (int t = 0; t < nq; ++t)
           for (int c = 0; c < NH; ++c)
-            tma_load_3d(base + (uint32_t)(t * NH + c) * kHalf, &tmq, bar(kBarQ), c * 64, h * G,
-                        (2 * pair + t) * (kRows / G));
+            tma_load_3d(base + (uint32_t)(t * NH + c) * kHalf, &tmq, bar(kBarQ), c * 64,
+                        wk.s.h * G, (2 * wk.s.pair + t) * (kRows / G));
       }
-      const int streams = two ? 1 : 2;
+      const int streams = wk.s.two ? 1 : 2;
       auto entry = [&](int t, int i) -> int {  // lane l < 8: page l's block
-        const int pg = block_of(t, i) * kPages + lane;
-        return lane < kPages && i < count_of(t) && pg < p.npb ? p.prefix_blocks[pg] : 0;
+        const int pg = wk.block(t, i) * kPages + lane;
+        return lane < kPages && t < streams && i < wk.count(t) && pg < p.npb
+                   ? p.prefix_blocks[pg] : 0;
       };
-      int cur[2] = {entry(0, 0), two ? 0 : entry(1, 0)};
-      bool ok = true;
-      for (int i = 0; ok && i < count_of(0); ++i) {
-        const int nxt[2] = {entry(0, i + 1), two ? 0 : entry(1, i + 1)};
+      int cur0 = entry(0, 0), cur1 = entry(1, 0);
+      for (int i = 0; ok && i < wk.count(0); ++i) {
+        const int nxt0 = entry(0, i + 1), nxt1 = entry(1, i + 1);
         for (int v = 0; ok && v < 2; ++v) {  // K of the streams, then V
           for (int t = 0; t < streams; ++t) {
-            if (i >= count_of(t)) continue;
-            const int j = block_of(t, i), bb = buf_of(t, i), u = use_of(i);
-            const int npg = min(kPages, p.npb - j * kPages);
-            int blk = t == 0 ? cur[0] : cur[1];
+            if (i >= wk.count(t)) continue;
+            const int bb = wk.buf(t, i), u = wk.use(t, i);
+            const int npg = min(kPages, p.npb - wk.block(t, i) * kPages);
+            int blk = t == 0 ? cur0 : cur1;
             if (lane < npg && (blk < 0 || blk >= p.NB)) {  // read as zeros, past the pool
               if (v == 0) report_error(p.err_word, PKV_ERR_BOUNDS);
               blk = p.NB;
@@ -178,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < npg) {
               const uint32_t dst = base + (v ? kOffV : kOffK) + (uint32_t)bb * NH * kHalf +
                                    (uint32_t)lane * kPageSize * 128;
-              const int r = (blk * p.Hkv + h) * kPageSize;
+              const int r = (blk * p.Hkv + wk.s.h) * kPageSize;
               for (int c = 0; c < NH; ++c)
                 tma_load_2d_plain(dst + (uint32_t)c * kHalf,
                                   v ? (const void*)&tmv : (const void*)&tmk, bar(full), c * 64, r);
@@ -186,13 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ok = ok && !__any_sync(0xffffffffu, *abort_flag != 0);
-        cur[0] = nxt[0];
-        cur[1] = nxt[1];
+        cur0 = nxt0;
+        cur1 = nxt1;
       }
+      wk.done();
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0 && nblk > 0) {
+    if (lane == 0) {
       constexpr uint32_t kIdS = idesc_f16(BF16, false, kRows, kTok);
       constexpr uint32_t kIdO = idesc_f16(BF16, true, kRows, D);
       auto commit = [&](int i) {
@@ -203,18 +289,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk = sdesc(base + kOffK, 16, 1024);
       const uint64_t dv = sdesc(base + kOffV, kHalf, 1024);
       auto qk = [&](int t, int i) {
-        const uint64_t a0 = dq + ((uint64_t)(two ? t : 0) * NH * kHalf >> 4);
-        const uint64_t b0 = dk + ((uint64_t)buf_of(t, i) * NH * kHalf >> 4);
+        const uint64_t a0 = dq + ((uint64_t)(wk.s.two ? t : 0) * NH * kHalf >> 4);
+        const uint64_t b0 = dk + ((uint64_t)wk.buf(t, i) * NH * kHalf >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32;
           umma(tmem + (uint32_t)t * kTok, a0 + (off >> 4), b0 + (off >> 4), kIdS, ks > 0);
         }
         commit(kBarSFull + t);
-        if (!two || t == 1) commit(kBarKFree + buf_of(t, i));
+        if (!wk.s.two || t == 1) commit(kBarKFree + wk.buf(t, i));
       };
       auto pv = [&](int t, int i) {  // P_t: per 64 tokens 32 columns of hi, then 32 of lo pairs
-        const uint64_t b0 = dv + ((uint64_t)buf_of(t, i) * NH * kHalf >> 4);
+        const uint64_t b0 = dv + ((uint64_t)wk.buf(t, i) * NH * kHalf >> 4);
         const uint32_t pt = tmem + (uint32_t)t * kTok;
         const uint32_t dt = tmem + 256 + (uint32_t)t * D;
 #pragma unroll
@@ -225,54 +311,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_ts(dt, pa + 32, bv, kIdO, 1);
         }
         commit(kBarODone + t);
-        if (!two || t == 1) commit(kBarVFree + buf_of(t, i));
+        if (!wk.s.two || t == 1) commit(kBarVFree + wk.buf(t, i));
       };
-      bool ok = wait(kBarQ, 0);
-      for (int t = 0; ok && t < 2; ++t) {
-        if (count_of(t) == 0) continue;
-        ok = wait(kBarKFull + buf_of(t, 0), 0);
-        if (!ok) break;
-        tc_fence_after();
-        qk(t, 0);
-      }
-      for (int i = 0; ok && i < count_of(0); ++i) {
+      bool ok = true;
+      uint32_t parts = 0;
+      // The first product over O_t of a part comes after P_t, which the softmax
+      // threads hand over after they have read the last part's O_t out.
+      while (ok && next_part(line, at, hi, wk.s)) {
+        ok = wait(kBarQ, parts++ & 1);
         for (int t = 0; ok && t < 2; ++t) {
-          if (i >= count_of(t)) continue;
-          ok = wait(kBarPFull + t, (uint32_t)(i & 1)) &&
-               wait(kBarVFull + buf_of(t, i), (uint32_t)(use_of(i) & 1));
+          if (wk.count(t) == 0) continue;
+          ok = wait(kBarKFull + wk.buf(t, 0), (uint32_t)(wk.use(t, 0) & 1));
           if (!ok) break;
           tc_fence_after();
-          pv(t, i);
-          if (i + 1 < count_of(t)) {
-            ok = wait(kBarKFull + buf_of(t, i + 1), (uint32_t)(use_of(i + 1) & 1));
+          qk(t, 0);
+        }
+        for (int i = 0; ok && i < wk.count(0); ++i) {
+          for (int t = 0; ok && t < 2; ++t) {
+            if (i >= wk.count(t)) continue;
+            ok = wait(kBarPFull + t, (uint32_t)((wk.str(t) + i) & 1)) &&
+                 wait(kBarVFull + wk.buf(t, i), (uint32_t)(wk.use(t, i) & 1));
             if (!ok) break;
-            qk(t, i + 1);
+            tc_fence_after();
+            pv(t, i);
+            if (i + 1 < wk.count(t)) {
+              ok = wait(kBarKFull + wk.buf(t, i + 1), (uint32_t)(wk.use(t, i + 1) & 1));
+              if (!ok) break;
+              qk(t, i + 1);
+            }
           }
         }
+        wk.done();
       }
     }
   } else {
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2;           // stream
     const int tt = tid - t * kRows;    // row in the tile
-    const int nt = count_of(t);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + (uint32_t)t * kTok + lane_base;
     const uint32_t t_o = tmem + 256 + (uint32_t)t * D + lane_base;
-    const int row = (2 * pair + (two ? t : 0)) * kRows + tt;
-    const int b = row / G;
-    // last position the row sees; rows past the batch (zero q) see all, unused
-    const int vis = (b < p.B ? ctx_of(b) : seen) - 1;
-    const int all_vis = __reduce_min_sync(0xffffffffu, vis);
     const float c2 = p.scale_log2;
-    float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
     uint32_t r[32];
+    while (ok && next_part(line, at, hi, wk.s)) {
+    const int nt = wk.count(t), done = wk.str(t);
+    const int row = (2 * wk.s.pair + (wk.s.two ? t : 0)) * kRows + tt;
+    const int b = row / G;
+    // last position the row sees; rows past the batch (zero q) see all, unused
+    const int vis = (b < p.B ? prefix_len(p.context_lens[b], p) : seen) - 1;
+    const int all_vis = __reduce_min_sync(0xffffffffu, vis);
+    float m_ref = -INFINITY, l_sum = 0.f;
     for (int i = 0; i < nt; ++i) {
-      ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)(i & 1)));
+      ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
       if (!ok) break;
       tc_fence_after();
-      const int tok0 = block_of(t, i) * kTok;
+      const int tok0 = wk.block(t, i) * kTok;
       const bool full = tok0 + kTok - 1 <= all_vis;
       uint32_t sa[32], sb[32];
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -314,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l_sum *= alpha;
       }
       if (i > 0) {
-        ok = __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((i - 1) & 1)));
+        ok = __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + i - 1) & 1)));
         if (!ok) break;
         tc_fence_after();
         if (__any_sync(0xffffffffu, grow)) {
@@ -380,9 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // V rows that no sequence sees may hold anything (0 x NaN): zeroed in the
       // staged block by the stream that uses it first
-      if (tok0 + kTok > seen && (t == 0 || !two)) {
-        const int bb = buf_of(t, i);
-        ok = __all_sync(0xffffffffu, wait(kBarVFull + bb, (uint32_t)(use_of(i) & 1)));
+      if (tok0 + kTok > seen && (t == 0 || !wk.s.two)) {
+        const int bb = wk.buf(t, i);
+        ok = __all_sync(0xffffffffu, wait(kBarVFull + bb, (uint32_t)(wk.use(t, i) & 1)));
         if (!ok) break;
         const int first = max(0, seen - tok0);
         const uint32_t vb = base + kOffV + (uint32_t)bb * NH * kHalf;
@@ -399,28 +493,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBarPFull + t));
     }
     // ---- the stream's partial: m, l and the unnormalised o of its rows
-    if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((nt - 1) & 1)));
-    const int64_t slot = ((int64_t)(h * p.pairs + pair) * 2) * p.splits +
-                         (two ? t * p.splits + split : 2 * split + t);
-    if (b < p.B) {
-      const bool any = ok && nt > 0 && l_sum != 0.f;  // NaN counts: it has to show
-      reinterpret_cast<float2*>(p.part_ml)[slot * kRows + tt] =
-          any ? make_float2(m_ref, l_sum) : make_float2(-INFINITY, 0.f);
-    }
-    if (ok && nt > 0) {
+    if (ok && nt > 0)
+      ok = __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + nt - 1) & 1)));
+    if (!ok) break;
+    const int64_t slot = ((int64_t)blockIdx.x + wk.s.pair * p.Hkv + wk.s.h) * 2 + t;
+    const bool any = nt > 0 && l_sum != 0.f;  // NaN counts: it has to show
+    if (b < p.B) p.pre_ml[slot * kRows + tt] = any ? make_float2(m_ref, l_sum)
+                                                   : make_float2(-INFINITY, 0.f);
+    if (nt > 0) {
       tc_fence_after();
-      float* po = p.part_o + (slot * kRows + tt) * D;
+      float* po = p.pre_o + (slot * kRows + tt) * D;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         tmem_ld32(t_o + (uint32_t)cc * 32, r);
         if (b < p.B) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<float4*>(po + cc * 32)[e] =
-                make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                            __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+          for (int e = 0; e < 4; ++e)  // 32 bytes at once: whole sectors
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             po + cc * 32 + 8 * e),
+                         "r"(r[8 * e]), "r"(r[8 * e + 1]), "r"(r[8 * e + 2]), "r"(r[8 * e + 3]),
+                         "r"(r[8 * e + 4]), "r"(r[8 * e + 5]), "r"(r[8 * e + 6]),
+                         "r"(r[8 * e + 7])
+                         : "memory");
         }
       }
+      tc_fence_before();  // O_t is read before P_t of the next part is handed over
+    }
+    wk.done();
     }
   }
 
@@ -438,109 +537,423 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ---- the merge: one CTA of kMergeWarps warps per row; a warp's 32 lanes hold
-// the row's d columns (two or four each) and take every kMergeWarps-th partial
-constexpr int kMergeWarps = 4;
+// ---- own parts: 16-bit pages on warp-level MMAs, as in the decode kernel
+constexpr int kOwnRing = 3;  // K+V page slots: 24 KB at d 128, what the prefix kernel leaves free
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixMergeParams p) {
+struct OwnPlan {
+  static constexpr int kTile = kPageSize * D * 2;  // one K (or V) page
+  static constexpr int kStage = 2 * kTile;
+  static constexpr size_t kSmem = 1024 + kOwnRing * kStage + 8 * kOwnRing;
+};
+
+template <bool BF16, int D, int G>
+__global__ void __launch_bounds__(32)
+    own_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tmk,
+               const __grid_constant__ CUtensorMap tmv) {
+  using PL = OwnPlan<D>;
+  constexpr int kMT = D / 16, kBoxes = D * 2 / 128;
+  const int lane = threadIdx.x;
+  const int chunk = blockIdx.x % p.chunks, seg = blockIdx.x / p.chunks;
+  const int b = seg / p.Hkv, h = seg - b * p.Hkv;
+  // The kernel before this one reads and writes nothing that matters here, and
+  // everything earlier is complete (it waits before it lets this one start).
+  // The merge behind waits for this kernel alone, so one CTA ends after both.
+  auto leave = [&] {
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+  const int ctx = p.context_lens[b];
+  if (ctx < 0 || ctx > p.MBS * kPageSize) {
+    if (lane == 0 && chunk == 0 && h == 0) report_error(p.err_word, PKV_ERR_BOUNDS);
+    leave();
+    return;
+  }
+  const int np = (ctx + kPageSize - 1) / kPageSize;
+  const int first = p.npb + chunk * p.chunk_pages;
+  const int n = (chunk == p.chunks - 1 ? np : min(np, first + p.chunk_pages)) - first;
+  if (n <= 0) {
+    leave();
+    return;
+  }
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bars = ring + kOwnRing * PL::kStage;
+  if (lane == 0) {
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+    for (int s = 0; s < kOwnRing; ++s) mbar_init(bars + 8 * s, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const int32_t* table = p.block_tables + (int64_t)b * p.MBS + first;
+  // page j's TMA row sits in lane j % 32, 32 pages looked up at a time
+  auto look_up = [&](int j0) -> int {
+    const int j = j0 + lane;
+    if (j >= n) return -1;
+    const int blk = table[j];
+    if (blk >= 0 && blk < p.NB) return (blk * p.Hkv + h) * kPageSize;
+    report_error(p.err_word, PKV_ERR_BOUNDS);
+    return -1;
+  };
+  int cur = look_up(0), nxt = n > 32 ? look_up(32) : -1;  // of pages 32 k .., 32 (k + 1) ..
+  int group = 0;
+  auto row_of = [&](int j) -> int {  // j / 32 is group or group + 1
+    const int a = __shfl_sync(0xffffffffu, cur, j & 31), c = __shfl_sync(0xffffffffu, nxt, j & 31);
+    return (j >> 5) == group ? a : c;
+  };
+  const uint64_t pol = l2_policy_evict_first();
+  auto issue = [&](int j) {
+    const int row = row_of(j);
+    if (lane == 0) {
+      const int s = j % kOwnRing;
+      const uint32_t kt = ring + (uint32_t)(s * PL::kStage), bar = bars + 8 * s;
+      if (row >= 0) {
+        mbar_arrive_expect_tx(bar, PL::kStage);
+#pragma unroll
+        for (int bx = 0; bx < kBoxes; ++bx) {
+          tma_load_2d(kt + bx * kPageSize * 128, &tmk, bar, bx * 64, row, pol);
+          tma_load_2d(kt + PL::kTile + bx * kPageSize * 128, &tmv, bar, bx * 64, row, pol);
+        }
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+  };
+  int issued = 0;
+  for (; issued < n && issued < kOwnRing; ++issued) issue(issued);
+
+  // fragment coordinates: see the decode kernel
+  const int c4 = lane & 3, r8 = lane >> 2;
+  const int qk_tok = (lane & 7) + ((lane >> 3) & 1) * 8, qk_hi = lane >> 4;
+  const int pv_tok = (lane & 7) + (lane >> 4) * 8, pv_hi = (lane >> 3) & 1;
+  auto swz = [](int tok, int chunk16) -> uint32_t {
+    return (uint32_t)((chunk16 >> 3) * (kPageSize * 128) + tok * 128 +
+                      (((chunk16 & 7) ^ (tok & 7)) << 4));
+  };
+  uint32_t qf[kMT][2];
+  {
+    const bool real = r8 < G;
+    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
+        static_cast<const uint16_t*>(p.q) + ((int64_t)b * p.Hq + h * G + (real ? r8 : 0)) * D);
+#pragma unroll
+    for (int ks = 0; ks < kMT; ++ks) {
+      qf[ks][0] = real ? qrow[8 * ks + c4] : 0;
+      qf[ks][1] = real ? qrow[8 * ks + c4 + 4] : 0;
+    }
+  }
+  float o[kMT][4], m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[mt][e] = 0.f;
+  const float c2 = p.scale_log2;
+
+  auto pages = [&](auto npc, const uint32_t* kt, const int* rem) {
+    constexpr int NP = decltype(npc)::value;
+    float x[NP][4];
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < kMT; ++ks) {
+        uint32_t a[4];
+        ldsm_x4(a, kt[i] + swz(qk_tok, 2 * ks + qk_hi));
+        if (ks & 1) mma_16816<BF16>(s1, a, qf[ks][0], qf[ks][1]);
+        else mma_16816<BF16>(s0, a, qf[ks][0], qf[ks][1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i][e] = (s0[e] + s1[e]) * c2;
+      if (rem[i] < kPageSize) {
+        if (r8 >= rem[i]) x[i][0] = x[i][1] = -INFINITY;
+        if (r8 + 8 >= rem[i]) x[i][2] = x[i][3] = -INFINITY;
+      }
+      mx0 = fmaxf(mx0, fmaxf(x[i][0], x[i][2]));
+      mx1 = fmaxf(mx1, fmaxf(x[i][1], x[i][3]));
+    }
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+    }
+    if (__any_sync(0xffffffffu, mx0 > m2[0] + 8.f || mx1 > m2[1] + 8.f)) {  // lazy rescale
+      const float n0 = fmaxf(m2[0], mx0), n1 = fmaxf(m2[1], mx1);
+      const float a0 = n0 == -INFINITY ? 1.f : ex2(m2[0] - n0);
+      const float a1 = n1 == -INFINITY ? 1.f : ex2(m2[1] - n1);
+      m2[0] = n0;
+      m2[1] = n1;
+      l2[0] *= a0;
+      l2[1] *= a1;
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt) {
+        o[mt][0] *= a0;
+        o[mt][1] *= a1;
+        o[mt][2] *= a0;
+        o[mt][3] *= a1;
+      }
+    }
+    const float mu0 = m2[0] == -INFINITY ? 0.f : m2[0], mu1 = m2[1] == -INFINITY ? 0.f : m2[1];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float p0 = ex2(x[i][0] - mu0), p1 = ex2(x[i][1] - mu1);
+      const float p2 = ex2(x[i][2] - mu0), p3 = ex2(x[i][3] - mu1);
+      l2[0] += p0 + p2;
+      l2[1] += p1 + p3;
+      const uint32_t h01 = pack2<BF16>(p0, p1), h23 = pack2<BF16>(p2, p3);
+      const float2 f01 = unpack2<BF16>(h01), f23 = unpack2<BF16>(h23);
+      const uint32_t l01 = pack2<BF16>(p0 - f01.x, p1 - f01.y);
+      const uint32_t l23 = pack2<BF16>(p2 - f23.x, p3 - f23.y);
+      const uint32_t vt = kt[i] + PL::kTile;
+      if (rem[i] < kPageSize) {  // rows of V past the end may hold anything (0 x NaN)
+        const int nz = (kPageSize - rem[i]) * kBoxes * 8;
+        for (int e = lane; e < nz; e += 32) {
+          const int rr = rem[i] + e / (kBoxes * 8), bx = (e / 8) % kBoxes;
+          const uint32_t a = vt + (uint32_t)(bx * kPageSize * 128 + rr * 128 + (e % 8) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      const uint32_t bh0 = movm_trans(h01), bh1 = movm_trans(h23);
+      const uint32_t bl0 = movm_trans(l01), bl1 = movm_trans(l23);
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt) {
+        uint32_t a[4];
+        ldsm_x4_trans(a, vt + swz(pv_tok, 2 * mt + pv_hi));
+        mma_16816<BF16>(o[mt], a, bh0, bh1);
+        mma_16816<BF16>(o[mt], a, bl0, bl1);
+      }
+    }
+  };
+  auto ready = [&](int j) -> bool {
+    return mbar_wait_bounded(bars + 8 * (j % kOwnRing), (uint32_t)((j / kOwnRing) & 1), kWaitNs);
+  };
+  bool ok = true;
+  for (int j = 0; j < n;) {
+    const int k = n - j >= 2 ? 2 : 1;
+    uint32_t kt[2];
+    int rem[2];
+    bool valid = true;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i < k) {
+        ok = ok && __all_sync(0xffffffffu, ready(j + i));
+        kt[i] = ring + (uint32_t)((j + i) % kOwnRing) * PL::kStage;
+        rem[i] = min(kPageSize, ctx - (first + j + i) * kPageSize);
+        if (row_of(j + i) < 0) valid = false;
+      }
+    }
+    if (!ok) break;
+    if (k == 2 && valid) {
+      pages(Count<2>{}, kt, rem);
+    } else {
+      for (int i = 0; i < k; ++i)
+        if (row_of(j + i) >= 0) pages(Count<1>{}, kt + i, rem + i);
+    }
+    __syncwarp();
+    j += k;
+    // the look-up of the group after the one in nxt starts when j enters nxt
+    if ((j >> 5) != group && j < n) {
+      group = j >> 5;
+      cur = nxt;
+      nxt = (group + 1) * 32 < n ? look_up((group + 1) * 32) : -1;
+    }
+    for (; issued < n && issued < j + kOwnRing; ++issued) issue(issued);
+  }
+  if (!ok) {  // a copy never came: let those in flight land, then report
+    if (lane == 0) report_error(p.err_word, PKV_ERR_TIMEOUT);
+    for (int s = 0; s < kOwnRing; ++s) {
+      const int last = issued - 1 - s;
+      if (last >= 0) ready(last);
+    }
+    leave();
+    return;
+  }
+
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l2[0] += __shfl_xor_sync(0xffffffffu, l2[0], off);
+    l2[1] += __shfl_xor_sync(0xffffffffu, l2[1], off);
+  }
+  const int64_t slot = (int64_t)seg * p.chunks + chunk;
+  const int h0 = 2 * c4, h1 = h0 + 1;
+  if (r8 == 0) {
+    if (h0 < G) p.own_ml[slot * G + h0] = make_float2(m2[0], l2[0]);
+    if (h1 < G) p.own_ml[slot * G + h1] = make_float2(m2[1], l2[1]);
+  }
+  float* po = p.own_o + slot * G * D;
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt) {
+    const int dA = 16 * mt + r8;
+    if (h0 < G) {
+      po[h0 * D + dA] = o[mt][0];
+      po[h0 * D + dA + 8] = o[mt][2];
+    }
+    if (h1 < G) {
+      po[h1 * D + dA] = o[mt][1];
+      po[h1 * D + dA + 8] = o[mt][3];
+    }
+  }
+  leave();
+}
+
+// ---- the merge: WPR warps per row, kMergeWarps warps per CTA.  A warp's lanes
+// hold the row's d columns and take every WPR-th part, 4 loads in flight.
+constexpr int kMergeWarps = 4;
+template <int D, int WPR>
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
   constexpr int V = D / 32;  // columns per lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t orow = blockIdx.x;  // b Hq + hq
-  const int b = (int)(orow / p.Hq), hq = (int)(orow - (int64_t)b * p.Hq);
-  const int G = p.Hq / p.Hkv, h = hq / G;
-  const int row = b * G + hq - h * G, tile = row >> 7, pair = tile >> 1;
-  const bool two = (2 * pair + 1) * kRows < p.B * G;
-  const int n = two ? p.splits : 2 * p.splits;
-  const int64_t slot0 = ((int64_t)(h * p.pairs + pair) * 2) * p.splits +
-                        (two ? (tile & 1) * p.splits : 0);
-  const int rr = row & 127;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot0 * kRows + rr;
-  const float* po = p.part_o + (slot0 * kRows + rr) * D + lane * V;
-
-  // the common maximum over all parts (every warp for itself)
-  const float lse = p.lse[orow];  // the row's own part: log2 of its sum
-  float M = lse;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, ml[(int64_t)k * kRows].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float l = 0.f, acc[V];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const int64_t orow = (int64_t)blockIdx.x * (kMergeWarps / WPR) + warp / WPR;  // b Hq + hq
+  const bool real = orow < (int64_t)p.B * p.Hq;
+  float acc[V], l = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  if (M == -INFINITY) M = 0.f;  // nothing at all, or nothing but NaN
-  {
+  if (real) {
+    const int b = (int)(orow / p.Hq), hq = (int)(orow - (int64_t)b * p.Hq);
+    const int G = p.Hq / p.Hkv, h = hq / G, gi = hq - h * G;
+    // the row's parts: stream by stream of the prefix, then its own chunks
+    const int row = b * G + gi, tile = row >> 7, pair = tile >> 1, rr = row & 127;
+    const int seen = *p.seen;
+    int npre = 0, streams = 1;
+    int64_t pre0 = 0;
+    if (seen > 0) {
+      const Line line(p, seen);
+      const int w = line.weight(pair);
+      const int64_t s0 = line.start(pair, h);
+      const int64_t c0 = line.cta_of(s0), c1 = line.cta_of(s0 + (int64_t)(line.nblk - 1) * w);
+      streams = w == 2 ? 1 : 2;
+      npre = (int)(c1 - c0 + 1) * streams;
+      pre0 = (c0 + pair * p.Hkv + h) * 2 + (w == 2 ? tile & 1 : 0);
+    }
+    const int ctx = p.context_lens[b];
+    const int own = ctx < 0 || ctx > p.MBS * kPageSize
+                        ? 0 : max(0, (ctx + kPageSize - 1) / kPageSize - p.npb);
+    const int nown = min(p.chunks, (own + p.chunk_pages - 1) / p.chunk_pages);
+    const int64_t own0 = ((int64_t)(b * p.Hkv + h) * p.chunks) * G + gi;
+    const int n = npre + nown;
+    auto ml_of = [&](int k) -> float2 {
+      return k < npre ? p.pre_ml[(pre0 + (streams == 2 ? k : 2 * k)) * kRows + rr]
+                      : p.own_ml[own0 + (int64_t)(k - npre) * G];
+    };
+    auto o_of = [&](int k) -> const float* {
+      return (k < npre ? p.pre_o + ((pre0 + (streams == 2 ? k : 2 * k)) * kRows + rr) * D
+                       : p.own_o + (own0 + (int64_t)(k - npre) * G) * D) + lane * V;
+    };
+    float2 mine = make_float2(-INFINITY, 0.f);  // part `lane`
+    if (lane < n) mine = ml_of(lane);
+    float M = mine.x;
+    for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, ml_of(k).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.f;  // nothing at all, or nothing but NaN
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      if (k0 > 0) mine = k0 + lane < n ? ml_of(k0 + lane) : make_float2(-INFINITY, 0.f);
+      const float wl = ex2(mine.x - M);
+      const int m = min(32, n - k0);
 #pragma unroll 4
-    for (int k = warp; k < n; k += kMergeWarps) {
-      const float2 v = ml[(int64_t)k * kRows];
-      if (v.y != 0.f) {  // a part with nothing in it was not written
-        const float w = ex2(v.x - M);
-        l += w * v.y;
-        const float* x = po + (int64_t)k * kRows * D;
-        if constexpr (V == 4) {
-          const float4 o = *reinterpret_cast<const float4*>(x);
-          acc[0] += w * o.x;
-          acc[1] += w * o.y;
-          acc[2] += w * o.z;
-          acc[3] += w * o.w;
-        } else {
-          const float2 o = *reinterpret_cast<const float2*>(x);
-          acc[0] += w * o.x;
-          acc[1] += w * o.y;
+      for (int k = sub; k < m; k += WPR) {
+        const float w = __shfl_sync(0xffffffffu, wl, k), ll = __shfl_sync(0xffffffffu, mine.y, k);
+        if (ll != 0.f) {  // a part with nothing in it was not written
+          l += w * ll;
+          const float* x = o_of(k0 + k);
+          if constexpr (V == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(x);
+            acc[0] += w * v.x;
+            acc[1] += w * v.y;
+            acc[2] += w * v.z;
+            acc[3] += w * v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(x);
+            acc[0] += w * v.x;
+            acc[1] += w * v.y;
+          }
         }
       }
     }
-    if (warp == 0 && lse != -INFINITY) {
-      const float w = ex2(lse - M);
-      l += w;
-      const float* x = p.own_o + orow * D + lane * V;
+  }
+  if constexpr (WPR > 1) {
+    __shared__ float sh[kMergeWarps][D + 1];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += w * x[e];
+    for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
+    if (lane == 0) sh[warp][D] = l;
+    __syncthreads();
+    if (sub != 0) return;
+    for (int w = 1; w < WPR; ++w) {
+      l += sh[warp + w][D];
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += sh[warp + w][lane * V + e];
     }
   }
-  __shared__ float sh[kMergeWarps][D + 1];
+  if (!real) return;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
-  if (lane == 0) sh[warp][D] = l;
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float o = 0.f, sum = 0.f;
+  for (int e = 0; e < V; ++e) acc[e] *= inv;
+  const int64_t at = orow * D + lane * V;
+  if (p.out_dtype == PKV_F32) {
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    o += sh[w][threadIdx.x];
-    sum += sh[w][D];
+    for (int e = 0; e < V; ++e) static_cast<float*>(p.out)[at + e] = acc[e];
+  } else {
+    const bool bf = p.out_dtype == PKV_BF16;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e)
+      out[e] = bf ? pack2<true>(acc[2 * e], acc[2 * e + 1])
+                  : pack2<false>(acc[2 * e], acc[2 * e + 1]);
   }
-  o = sum != 0.f ? o / sum : 0.f;
-  const int64_t at = orow * D + threadIdx.x;
-  if (p.out_dtype == PKV_F32) static_cast<float*>(p.out)[at] = o;
-  else if (p.out_dtype == PKV_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
-  else static_cast<__half*>(p.out)[at] = __float2half_rn(o);
+}
+
+// Every kernel may start before the one in front of it has ended (see the waits).
+template <typename... KP, typename... A>
+cudaError_t launch_behind(void (*kern)(KP...), unsigned grid, unsigned block, size_t smem,
+                          cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <bool BF16, int D>
 cudaError_t launch(const PrefixLaunch& l) {
-  auto kern = prefix_kernel<BF16, D>;
-  constexpr size_t smem = Plan<D>::kSmem;
+  const int G = l.p.Hq / l.p.Hkv;
+  auto pre = prefix_kernel<BF16, D>;
+  auto own = G == 1 ? own_kernel<BF16, D, 1> : G == 2 ? own_kernel<BF16, D, 2>
+             : G == 4 ? own_kernel<BF16, D, 4> : own_kernel<BF16, D, 8>;
   static std::atomic<uint64_t> configured{0};  // a bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (dev > 63 || !(configured.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(pre, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Plan<D>::kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(l.p.pairs * l.p.splits), (unsigned)l.p.Hkv, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = l.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, l.p, l.tmap_q, l.tmap_k, l.tmap_v);
+  static_assert(OwnPlan<D>::kSmem <= 48 * 1024, "no attribute needed");
+  const int64_t nblk = ((int64_t)l.p.npb * kPageSize + kTok - 1) / kTok;
+  const int last_w = (2 * l.p.pairs - 1) * kRows < l.p.B * G ? 2 : 1;
+  const int64_t cost = l.p.Hkv * nblk * (2 * (l.p.pairs - 1) + last_w);
+  e = launch_behind(pre, (unsigned)prefix_ctas(cost, l.p.ctas), kThreads, Plan<D>::kSmem, l.stream,
+                    l.p, l.tmap_q, l.tmap_k, l.tmap_v);
+  if (e != cudaSuccess) return e;
+  e = launch_behind(own, (unsigned)((int64_t)l.p.B * l.p.Hkv * l.p.chunks), 32, OwnPlan<D>::kSmem,
+                    l.stream, l.p, l.tmap_k, l.tmap_v);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)l.p.B * l.p.Hq;
+  if (rows >= kMergeRows)  // enough rows for every warp to have one of its own
+    return launch_behind(prefix_merge_kernel<D, 1>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps),
+                         kMergeWarps * 32, 0, l.stream, l.p);
+  return launch_behind(prefix_merge_kernel<D, kMergeWarps>, (unsigned)rows, kMergeWarps * 32, 0,
+                       l.stream, l.p);
 }
 
 }  // namespace px
@@ -549,20 +962,6 @@ cudaError_t launch_prefix(const PrefixLaunch& l) {
   if (l.d == 64) return l.bf16 ? px::launch<true, 64>(l) : px::launch<false, 64>(l);
   if (l.d == 128) return l.bf16 ? px::launch<true, 128>(l) : px::launch<false, 128>(l);
   return cudaErrorNotSupported;
-}
-
-cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int d, cudaStream_t stream) {
-  auto kern = d == 64 ? px::prefix_merge_kernel<64> : px::prefix_merge_kernel<128>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.Hq), 1, 1);
-  cfg.blockDim = dim3(px::kMergeWarps * 32, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace pkv
