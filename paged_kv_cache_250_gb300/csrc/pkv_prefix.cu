@@ -70,7 +70,7 @@ template <int N>
 struct Count {
   static constexpr int value = N;
 };
-constexpr int64_t kMergeRows = 1024;
+constexpr int64_t kMergeRows = 1024, kMergeParts = 8;
 
 // tokens of the prefix that a sequence of length c sees (bad lengths: none; the
 // own kernel reports them)
@@ -93,8 +93,8 @@ struct Line {
   __device__ int64_t start(int pair, int h) const {
     return (int64_t)Hkv * nblk * 2 * pair + (int64_t)h * nblk * weight(pair);
   }
-  __device__ int64_t share(int64_t c) const { return (c * cost + n - 1) / n; }  // first cost of CTA c
-  __device__ int64_t cta_of(int64_t x) const { return x * n / cost; }
+  __device__ int64_t share(int64_t c) const { return udiv64(c * cost + n - 1, n); }  // first cost of CTA c
+  __device__ int64_t cta_of(int64_t x) const { return udiv64(x * n, cost); }
 };
 // One CTA's blocks of one segment.
 struct Part {
@@ -106,11 +106,11 @@ struct Part {
 __device__ __forceinline__ bool next_part(const Line& ln, int64_t& x, int64_t hi, Part& s) {
   while (x < hi) {
     const int64_t per = (int64_t)ln.Hkv * ln.nblk * 2;
-    s.pair = (int)min(x / per, (int64_t)(ln.pairs - 1));
+    s.pair = (int)min(udiv64(x, per), (int64_t)(ln.pairs - 1));
     const int w = ln.weight(s.pair);
     s.two = w == 2;
     const int64_t seg = (int64_t)ln.nblk * w;
-    s.h = (int)((x - per * s.pair) / seg);
+    s.h = (int)udiv64(x - per * s.pair, seg);
     const int64_t s0 = ln.start(s.pair, s.h);
     s.j0 = (int)((x - s0 + w - 1) / w);
     const int64_t j1 = min((int64_t)ln.nblk, (hi - s0 + w - 1) / w);
@@ -133,11 +133,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = p.Hq / p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the kernel behind this one reads nothing that this one writes before its
-  // own end, and everything earlier is complete: it may start
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -153,6 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
+    prefetch_tmap(&tmq);
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
     *abort_flag = 0;
     *max_len = 0;
     for (int i = 0; i < kNumBars; ++i) {
@@ -165,6 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+
+  // so far nothing of the kernel in front was needed, and it may still run
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the kernel behind this one reads nothing that this one writes before its
+  // own end, and everything earlier is complete: it may start
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the positions any sequence sees of the prefix: rows of V behind them may
   // never have been written
@@ -288,30 +292,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = sdesc(base, 16, 1024);
       const uint64_t dk = sdesc(base + kOffK, 16, 1024);
       const uint64_t dv = sdesc(base + kOffV, kHalf, 1024);
-      auto qk = [&](int t, int i) {
-        const uint64_t a0 = dq + ((uint64_t)(wk.s.two ? t : 0) * NH * kHalf >> 4);
-        const uint64_t b0 = dk + ((uint64_t)wk.buf(t, i) * NH * kHalf >> 4);
+      // bb: the buffer; last: nothing uses the buffer after this
+      auto qk = [&](int t, int bb, bool two, bool last) {
+        const uint64_t a0 = dq + (two && t ? (uint64_t)NH * kHalf >> 4 : 0ull);
+        const uint64_t b0 = dk + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32;
           umma(tmem + (uint32_t)t * kTok, a0 + (off >> 4), b0 + (off >> 4), kIdS, ks > 0);
         }
         commit(kBarSFull + t);
-        if (!wk.s.two || t == 1) commit(kBarKFree + wk.buf(t, i));
+        if (last) commit(kBarKFree + bb);
       };
-      auto pv = [&](int t, int i) {  // P_t: per 64 tokens 32 columns of hi, then 32 of lo pairs
-        const uint64_t b0 = dv + ((uint64_t)wk.buf(t, i) * NH * kHalf >> 4);
+      auto pv = [&](int t, int bb, bool add, bool last) {  // P_t: per 64 tokens 32 columns of hi, then 32 of lo pairs
+        const uint64_t b0 = dv + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
         const uint32_t pt = tmem + (uint32_t)t * kTok;
         const uint32_t dt = tmem + 256 + (uint32_t)t * D;
 #pragma unroll
         for (int ks = 0; ks < kTok / 16; ++ks) {
           const uint64_t bv = b0 + ((uint32_t)ks * 16 * 128 >> 4);
           const uint32_t pa = pt + (uint32_t)(ks >> 2) * 64 + (uint32_t)(ks & 3) * 8;
-          umma_ts(dt, pa, bv, kIdO, i > 0 || ks > 0);
+          umma_ts(dt, pa, bv, kIdO, add || ks > 0);
           umma_ts(dt, pa + 32, bv, kIdO, 1);
         }
         commit(kBarODone + t);
-        if (!wk.s.two || t == 1) commit(kBarVFree + wk.buf(t, i));
+        if (last) commit(kBarVFree + bb);
       };
       bool ok = true;
       uint32_t parts = 0;
@@ -319,25 +324,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       // threads hand over after they have read the last part's O_t out.
       while (ok && next_part(line, at, hi, wk.s)) {
         ok = wait(kBarQ, parts++ & 1);
-        for (int t = 0; ok && t < 2; ++t) {
-          if (wk.count(t) == 0) continue;
-          ok = wait(kBarKFull + wk.buf(t, 0), (uint32_t)(wk.use(t, 0) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          qk(t, 0);
-        }
-        for (int i = 0; ok && i < wk.count(0); ++i) {
-          for (int t = 0; ok && t < 2; ++t) {
-            if (i >= wk.count(t)) continue;
-            ok = wait(kBarPFull + t, (uint32_t)((wk.str(t) + i) & 1)) &&
-                 wait(kBarVFull + wk.buf(t, i), (uint32_t)(wk.use(t, i) & 1));
+        if (wk.s.two) {  // one buffer after the other, both streams from it
+          const int n = wk.s.nblk;
+          uint32_t u0 = (uint32_t)wk.buf0, u1 = (uint32_t)wk.buf1;  // uses of the next block's
+          const uint32_t st = (uint32_t)wk.str0, st1 = (uint32_t)wk.str1;
+          ok = ok && wait(kBarKFull, u0 & 1);
+          if (ok) {
+            tc_fence_after();
+            qk(0, 0, true, false);
+            qk(1, 0, true, true);
+          }
+          for (int i = 0; ok && i < n; ++i) {
+            const int bb = i & 1;
+            const bool more = i + 1 < n;
+            const uint32_t vu = bb ? u1 : u0, ku = bb ? u0 + 1 : u1;  // this V, the next K
+            if (!(ok = wait(kBarPFull, (st + i) & 1) && wait(kBarVFull + bb, vu & 1))) break;
+            tc_fence_after();
+            pv(0, bb, i > 0, false);
+            if (more) {
+              if (!(ok = wait(kBarKFull + (bb ^ 1), ku & 1))) break;
+              qk(0, bb ^ 1, true, false);
+            }
+            if (!(ok = wait(kBarPFull + 1, (st1 + i) & 1))) break;
+            tc_fence_after();
+            pv(1, bb, i > 0, true);
+            if (more) qk(1, bb ^ 1, true, true);
+            if (bb) {
+              ++u0;
+              ++u1;
+            }
+          }
+        } else {  // stream t from buffer t
+          const int n0 = wk.count(0), n1 = wk.count(1);
+          const uint32_t u[2] = {(uint32_t)wk.buf0, (uint32_t)wk.buf1};
+          const uint32_t st[2] = {(uint32_t)wk.str0, (uint32_t)wk.str1};
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == 1 && n1 == 0) break;
+            ok = ok && wait(kBarKFull + t, u[t] & 1);
             if (!ok) break;
             tc_fence_after();
-            pv(t, i);
-            if (i + 1 < wk.count(t)) {
-              ok = wait(kBarKFull + wk.buf(t, i + 1), (uint32_t)(wk.use(t, i + 1) & 1));
+            qk(t, t, false, true);
+          }
+          for (int i = 0; ok && i < n0; ++i) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (i >= (t ? n1 : n0)) break;
+              ok = wait(kBarPFull + t, (st[t] + i) & 1) && wait(kBarVFull + t, (u[t] + i) & 1);
               if (!ok) break;
-              qk(t, i + 1);
+              tc_fence_after();
+              pv(t, t, i > 0, true);
+              if (i + 1 < (t ? n1 : n0)) {
+                ok = wait(kBarKFull + t, (u[t] + i + 1) & 1);
+                if (!ok) break;
+                qk(t, t, false, true);
+              }
             }
           }
         }
@@ -356,17 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t r[32];
     while (ok && next_part(line, at, hi, wk.s)) {
     const int nt = wk.count(t), done = wk.str(t);
+    int tok0 = wk.block(t, 0) * kTok;
+    const int tok_step = wk.s.two ? kTok : 2 * kTok;
     const int row = (2 * wk.s.pair + (wk.s.two ? t : 0)) * kRows + tt;
     const int b = row / G;
     // last position the row sees; rows past the batch (zero q) see all, unused
     const int vis = (b < p.B ? prefix_len(p.context_lens[b], p) : seen) - 1;
     const int all_vis = __reduce_min_sync(0xffffffffu, vis);
     float m_ref = -INFINITY, l_sum = 0.f;
-    for (int i = 0; i < nt; ++i) {
+    for (int i = 0; i < nt; ++i, tok0 += tok_step) {
       ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
       if (!ok) break;
       tc_fence_after();
-      const int tok0 = wk.block(t, i) * kTok;
       const bool full = tok0 + kTok - 1 <= all_vis;
       uint32_t sa[32], sb[32];
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -803,6 +845,8 @@ constexpr int kMergeWarps = 4;
 template <int D, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
   constexpr int V = D / 32;  // columns per lane
+  // a kernel behind this one that waits for its end may start its prologue
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
   const int64_t orow = (int64_t)blockIdx.x * (kMergeWarps / WPR) + warp / WPR;  // b Hq + hq
@@ -852,7 +896,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
       if (k0 > 0) mine = k0 + lane < n ? ml_of(k0 + lane) : make_float2(-INFINITY, 0.f);
       const float wl = ex2(mine.x - M);
       const int m = min(32, n - k0);
-#pragma unroll 4
+#pragma unroll 8
       for (int k = sub; k < m; k += WPR) {
         const float w = __shfl_sync(0xffffffffu, wl, k), ll = __shfl_sync(0xffffffffu, mine.y, k);
         if (ll != 0.f) {  // a part with nothing in it was not written
@@ -949,7 +993,9 @@ cudaError_t launch(const PrefixLaunch& l) {
                     l.stream, l.p, l.tmap_k, l.tmap_v);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)l.p.B * l.p.Hq;
-  if (rows >= kMergeRows)  // enough rows for every warp to have one of its own
+  // a warp per row where rows are many and their parts few
+  const int64_t segs = (int64_t)l.p.pairs * l.p.Hkv;
+  if (rows >= kMergeRows && l.p.ctas < kMergeParts * segs)
     return launch_behind(prefix_merge_kernel<D, 1>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps),
                          kMergeWarps * 32, 0, l.stream, l.p);
   return launch_behind(prefix_merge_kernel<D, kMergeWarps>, (unsigned)rows, kMergeWarps * 32, 0,
