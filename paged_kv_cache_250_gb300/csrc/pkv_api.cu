@@ -228,11 +228,17 @@ SharedLayout shared_layout(const pkv_cache_desc* d, int32_t batch, int sms) {
   return s;
 }
 
-// Whether the prefix is worth a pass of its own; otherwise every sequence reads
-// it through the prefix table, one launch in place of three.
+// Whether the prefix is worth a pass of its own.  Otherwise one kernel reads it
+// for every sequence, from L2 after the first, which takes 12 to 16 us and 0.1 us
+// per MB read again; the three kernels take 12 to 16 us with a prefix of up to
+// 1024 tokens, the prefix's one pass on top of that when it is longer, and more
+// of the host's time (14 against 8 us).  Measured, one kernel against three, 32/8
+// heads of 128: 4 x 4096 tokens 16.9 / 16.9 us, 8 x 1024 13.8 / 13.3, 32 x 256
+// 17.5 / 15.6, 8 x 4096 22 / 17, 64 x 4096 106 / 28; two sequences never gain
+// (2 x 16384: 24 / 29).
 bool shared_pays(const pkv_cache_desc* d, int32_t batch, int32_t npb) {
-  (void)d;
-  return batch > 1 && npb > 0;
+  const int64_t again = (int64_t)(batch - 1) * npb * kPageSize * d->num_kv_heads * d->head_dim * 4;
+  return batch >= 4 && again >= (int64_t)32 << 20;
 }
 
 pkv_status append_checks(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,

@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // and CTA c owns the units with c T / Gs <= X(x) < (c+1) T / Gs, T the total
   // cost, Gs the CTAs given work (each about kRangeMin pages or more).
   const int64_t Tc = W + (int64_t)p.Hkv * kSegCost * nzp[p.B];
-  const int64_t Gs_raw = (Tc + kRangeMin - 1) / kRangeMin;
+  constexpr int kMin = MODE == kModePlain ? kRangeMin : kRangeMinFine;
+  const int64_t Gs_raw = (Tc + kMin - 1) / kMin;
   const int64_t Gs = Gs_raw < Gn ? (Gs_raw > 0 ? Gs_raw : 1) : Gn;
   auto seq_cost0 = [&](int b) -> int64_t {
     return (int64_t)p.Hkv * (pfx[b] + (int64_t)kSegCost * nzp[b]);
@@ -895,6 +896,9 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // (against a running maximum for up to four partials, else against their
   // common maximum), so the result is bitwise the same whichever form runs.
   // No shared memory, no barrier.
+  // a partial with something in it; beside the plain form a NaN sum counts too,
+  // so that a NaN a row sees shows in its output however the row was cut
+  auto filled = [](float l) -> bool { return MODE == kModePlain ? l > 0.f : l != 0.f; };
   auto merge_cols = [&](int seg, int t, int T) {
     const int b = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;
     const int64_t np = pfx[b + 1] - pfx[b];
@@ -920,7 +924,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
           if (kk < count) {
             const float2 v = __ldcg(ml + (int64_t)kk * NC);
             const float4 x = __ldcg(vo + (int64_t)kk * (NC * D / 4));
-            if (v.y > 0.f) {
+            if (filled(v.y)) {
               if (v.x > M) {
                 const float a = exp2f(M - v.x);  // 0 while nothing is summed
                 lsum *= a;
@@ -945,14 +949,14 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
 #pragma unroll 4
         for (int kk = 0; kk < count; ++kk) {
           const float2 v = __ldcg(ml + (int64_t)kk * NC);
-          if (v.y > 0.f) M = fmaxf(M, v.x);
+          if (filled(v.y)) M = fmaxf(M, v.x);
         }
         if (M > -INFINITY) {
 #pragma unroll 4
           for (int kk = 0; kk < count; ++kk) {
             const float2 v = __ldcg(ml + (int64_t)kk * NC);
             const float4 x = __ldcg(vo + (int64_t)kk * (NC * D / 4));
-            const float w = v.y > 0.f ? exp2f(v.x - M) : 0.f;
+            const float w = filled(v.y) ? exp2f(v.x - M) : 0.f;
             lsum += w * v.y;
             acc.x += w * x.x;
             acc.y += w * x.y;

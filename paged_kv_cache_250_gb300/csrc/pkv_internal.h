@@ -26,6 +26,14 @@ __host__ __device__ constexpr bool cache_is_fp8(CacheKind c) { return c == kCach
 // when the batch is small: a short context is not worth splitting) and is
 // walked in pieces of at most kRangeMax pages.
 constexpr int kRangeMin = 32;
+// The biased and shared-prefix forms of the single-token kernel cut finer: half
+// the work per CTA shortens small calls (one sequence of 701 tokens and 32 KV
+// heads 14.8 -> 12.4 us, 3000 tokens and 8 heads 15.8 -> 13.2, 32 sequences of
+// up to 100 tokens 18.2 -> 15.0) and leaves large ones, whose grid is full, as
+// they were (8: 11.5 us for the first, but 14.8 for the second); one sequence of
+// 8000 tokens with 4 heads, whose segments then merge 32 partials, takes 19.4
+// instead of 17.9.
+constexpr int kRangeMinFine = 16;
 constexpr int kRangeMax = 64;
 // Cost of starting a (sequence, KV head) segment, in pages, when shares are
 // cut (a state merge, an output write and a pipeline refill).
@@ -352,12 +360,18 @@ struct PrefixLaunch {
   int32_t d;
   cudaStream_t stream;
 };
-// CTAs of the prefix kernel with work: a share is at least two blocks of 128
-// tokens of a pair of row tiles (a block costs 2, or 1 where the second tile
-// is empty).
+// CTAs of the prefix kernel with work.  In units of a block of 128 tokens of a
+// pair of row tiles (cost 2; 1 where the second tile is empty, two of which run
+// side by side) the longest share is m = ceil(units / ctas); while m is small,
+// as many CTAs as shares of m take, no more: fewer partials in the same time
+// (64 sequences behind 8192 tokens, m = 4: 128 CTAs 41.1 us, 152 43.2).  A share
+// is at least one unit, so every CTA between a segment's first and last has a
+// part of it.
 __host__ __device__ inline int64_t prefix_ctas(int64_t cost, int32_t ctas) {
-  const int64_t most = cost / 4 > 0 ? cost / 4 : 1;
-  return most < ctas ? most : ctas;
+  const int64_t units = cost >> 1 > 0 ? cost >> 1 : 1;
+  for (int m = 1; m <= 4; ++m)
+    if (units <= (int64_t)m * ctas) return ((uint32_t)units + m - 1) / m;
+  return ctas;
 }
 cudaError_t launch_prefix(const PrefixLaunch& l);  // the three kernels
 

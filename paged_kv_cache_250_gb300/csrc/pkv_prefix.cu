@@ -106,14 +106,14 @@ struct Part {
 __device__ __forceinline__ bool next_part(const Line& ln, int64_t& x, int64_t hi, Part& s) {
   while (x < hi) {
     const int64_t per = (int64_t)ln.Hkv * ln.nblk * 2;
-    s.pair = (int)min(udiv64(x, per), (int64_t)(ln.pairs - 1));
+    s.pair = ln.pairs == 1 ? 0 : (int)min(udiv64(x, per), (int64_t)(ln.pairs - 1));
     const int w = ln.weight(s.pair);
     s.two = w == 2;
     const int64_t seg = (int64_t)ln.nblk * w;
     s.h = (int)udiv64(x - per * s.pair, seg);
     const int64_t s0 = ln.start(s.pair, s.h);
-    s.j0 = (int)((x - s0 + w - 1) / w);
-    const int64_t j1 = min((int64_t)ln.nblk, (hi - s0 + w - 1) / w);
+    s.j0 = (int)((x - s0 + w - 1) >> (w - 1));  // w is 1 or 2
+    const int64_t j1 = min((int64_t)ln.nblk, (hi - s0 + w - 1) >> (w - 1));
     s.nblk = (int)(j1 - s.j0);
     x = s0 + seg;
     if (s.nblk > 0) return true;
@@ -600,6 +600,8 @@ __global__ void __launch_bounds__(32)
   // The kernel before this one reads and writes nothing that matters here, and
   // everything earlier is complete (it waits before it lets this one start).
   // The merge behind waits for this kernel alone, so one CTA ends after both.
+  // (The merge may start once every CTA of this kernel has.)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto leave = [&] {
     if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
   };

@@ -117,6 +117,20 @@ def test_bad_blocks_and_lengths_are_reported():
     assert torch.all(o[1] == 0)
 
 
+@pytest.mark.parametrize("n", [40, 3000])
+def test_nan_shows_where_it_is_seen(n):
+    """A NaN in a key reaches every output of its sequence and KV head, whether
+    or not the sequence is cut over several CTAs, and nothing else."""
+    p = Paged([n, 200, n], 4, 2, 128, "bf16", 91)
+    q = p.queries(3, 92, 2.0)
+    p.kc[int(p.tables[0, n // 32]), 1, 2, 5] = float("nan")
+    o = decode(p, q, "f32", 30.0, alibi(4))
+    assert torch.isnan(o[0, 2:]).all()
+    ref, tol = expect_decode(p, q, 30.0, alibi(4))
+    check(o[1:], ref[1:], tol[1:], "f32")
+    check(o[0, :2], ref[0, :2], tol[0, :2], "f32")
+
+
 # ---------------------------------------------------------------- prefill
 def prefill(p, q, chunks, out="f32", cap=0.0, slopes=None, total=None):
     st = torch.tensor([0] + list(torch.tensor(chunks).cumsum(0)), dtype=torch.int32)
