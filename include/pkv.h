@@ -297,7 +297,8 @@ PKV_API pkv_status pkv_paged_decode_attention_window(
  *   s = scale q.k;  s = softcap tanh(s / softcap) if softcap > 0;
  *   s = s + alibi_slopes[hq] (u - t) if alibi_slopes is given.
  *   window, sinks as for pkv_paged_decode_attention_window (0: no window).
- *   softcap       0 (no cap), or between 2^-10 and 2^20.
+ *   softcap       0 (no cap), or between 2^-10 and 2^10.  The tanh is off by
+ *                 2^-22 of the cap at most.
  *   alibi_slopes  device fp32 [num_q_heads], or NULL.
  * With neither, the call is pkv_paged_decode_attention (or _window) itself.
  * Other arguments, workspace and guarantees as for

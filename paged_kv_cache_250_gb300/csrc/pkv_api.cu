@@ -196,10 +196,10 @@ pkv_status encode_q_map(CUtensorMap* map, const void* q, const pkv_cache_desc* d
              : PKV_ERR_CUDA;
 }
 
-// A cap is 0 (none) or between 2^-10 and 2^20: far outside the scores any
-// softmax separates, 2 / cap and the cap itself stay well inside fp32.
+// A cap is 0 (none) or between 2^-10 and 2^10: the tanh's error is 2^-22 of the
+// cap, and a wider cap bends no score that fp32 tells apart anyway.
 pkv_status bias_checks(float softcap, const float* slopes) {
-  if (softcap != 0.f && !(softcap >= 0x1p-10f && softcap <= 0x1p20f)) return PKV_ERR_INVALID_ARG;
+  if (softcap != 0.f && !(softcap >= 0x1p-10f && softcap <= 0x1p10f)) return PKV_ERR_INVALID_ARG;
   if (!aligned(slopes, 4)) return PKV_ERR_INVALID_ARG;
   return PKV_OK;
 }
@@ -386,12 +386,19 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
   if (form.mode == pkv::kModeShared) {
     e = l.cache == pkv::kCacheF16 ? pkv::launch_decode_shared_f16(l)
                                   : pkv::launch_decode_shared_bf16(l);
-  } else if (form.mode == pkv::kModeBiased) {
+  } else if (form.mode == pkv::kModeCap) {
     switch (l.cache) {
-      case pkv::kCacheF16: e = pkv::launch_decode_biased_f16(l); break;
-      case pkv::kCacheBF16: e = pkv::launch_decode_biased_bf16(l); break;
-      case pkv::kCacheE4M3: e = pkv::launch_decode_biased_e4m3(l); break;
-      default: e = pkv::launch_decode_biased_e4m3_tok(l); break;
+      case pkv::kCacheF16: e = pkv::launch_decode_cap_f16(l); break;
+      case pkv::kCacheBF16: e = pkv::launch_decode_cap_bf16(l); break;
+      case pkv::kCacheE4M3: e = pkv::launch_decode_cap_e4m3(l); break;
+      default: e = pkv::launch_decode_cap_e4m3_tok(l); break;
+    }
+  } else if (form.mode == pkv::kModeDist) {
+    switch (l.cache) {
+      case pkv::kCacheF16: e = pkv::launch_decode_dist_f16(l); break;
+      case pkv::kCacheBF16: e = pkv::launch_decode_dist_bf16(l); break;
+      case pkv::kCacheE4M3: e = pkv::launch_decode_dist_e4m3(l); break;
+      default: e = pkv::launch_decode_dist_e4m3_tok(l); break;
     }
   } else if (l.qcap == 1) {
     switch (l.cache) {
@@ -626,7 +633,8 @@ pkv_status pkv_paged_decode_attention_biased(
   st = bias_checks(softcap, alibi_slopes);
   if (st != PKV_OK) return st;
   DecodeForm form;
-  if (softcap > 0.f || alibi_slopes != nullptr) form.mode = pkv::kModeBiased;
+  if (softcap > 0.f) form.mode = pkv::kModeCap;
+  else if (alibi_slopes != nullptr) form.mode = pkv::kModeDist;
   form.softcap = softcap;
   form.slopes = alibi_slopes;
   return decode_impl(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
@@ -785,9 +793,7 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const void* k
   l.d = desc->head_dim;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
   if ((int64_t)batch * l.p.tiles_per_seq >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
-  const bool fine = softcap > pkv::kCapCoarse;
-  const cudaError_t e = fine              ? pkv::launch_prefill_cap_fine(l)
-                        : softcap > 0.f   ? pkv::launch_prefill_cap(l)
+  const cudaError_t e = softcap > 0.f       ? pkv::launch_prefill_cap(l)
                         : slopes != nullptr ? pkv::launch_prefill_dist(l)
                                             : pkv::launch_prefill(l);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

@@ -166,24 +166,15 @@ __device__ __forceinline__ float rcp(float x) {  // 1 / x (PTX rcp.approx; inf g
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// A score capped by a tanh, in log2 units.  With y = s / cap and
-// z = 2 y log2e,  tanh(y) = 1 - 2 / (1 + 2^z):  two special-function
-// instructions, and the ends come out as +-1 by themselves (2^z = inf or 0).
-// Its error is about 2^-22 of the CAP, whatever y is, so scores much smaller
-// than a wide cap lose bits; there (|y| < 0.25) the series
-// y (1 - y^2/3 + 2 y^4/15 - 17 y^6/315), off by at most 2^-21 of its value,
-// stands in.  `far` is the first form's result, cap_log2 = cap log2e.
-__device__ __forceinline__ float cap_near_zero(float z, float cap_log2, float far) {
-  const float y = z * 0.34657359027997264f;  // z ln2 / 2
-  const float w = y * y;
-  const float near = cap_log2 * y *
-                     fmaf(w, fmaf(w, fmaf(w, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-  return fabsf(y) < 0.25f ? near : far;
-}
-// x: the score in log2 units, z_of_x = 2 / cap
+// A score x capped by a tanh, both in log2 units: with y = s / cap and
+// z = 2 y log2e = x z_of_x (z_of_x = 2 / cap),  tanh(y) = 1 - 2 / (1 + 2^z):
+// two special-function instructions, and the ends come out as +-1 by themselves
+// (2^z = inf or 0).  The error is about 2^-22 of the cap, whatever y is: 2^-16
+// of a score's unit under a cap of 64, as much as a weight's own rounding to its
+// 16-bit pair.  (The series for small y would keep every bit under wide caps too;
+// it cost the E4M3 decode 9 % and the prefill kernel registers.)
 __device__ __forceinline__ float cap_score(float x, float z_of_x, float cap_log2) {
-  const float z = x * z_of_x;
-  return cap_near_zero(z, cap_log2, fmaf(rcp(1.f + ex2(z)), -2.f * cap_log2, cap_log2));
+  return fmaf(rcp(1.f + ex2(x * z_of_x)), -2.f * cap_log2, cap_log2);
 }
 
 // Two fp32 -> packed 16-bit pair (lo in the low half), round to nearest even.

@@ -143,8 +143,8 @@ struct DecodeParams {
   int32_t early_prologue;      // 1: read lengths/tables before waiting on the previous kernel
   int32_t trigger_next;        // 1: let the next kernel on the stream launch at once
   float scale_log2;            // softmax scale * log2(e)
-  // biased scores (MODE kModeBiased): cap log2e (0: no cap), 2 / cap, and one
-  // slope per query head (NULL: no distance bias)
+  // biased scores (MODE kModeDist, kModeCap): cap log2e, 2 / cap, and one slope
+  // per query head (NULL: no distance bias)
   float cap_log2, cap_z;
   const float* slopes;
   // a shared prefix (MODE kModeShared): the blocks of every sequence's first
@@ -152,8 +152,9 @@ struct DecodeParams {
   const int32_t* prefix_blocks;
   int32_t npb;
 };
-// Forms of the single-token kernel.
-constexpr int kModePlain = 0, kModeBiased = 1, kModeShared = 2;
+// Forms of the single-token kernel: distance bias alone, cap (with a distance
+// bias of zero slope or more), shared prefix.
+constexpr int kModePlain = 0, kModeDist = 1, kModeShared = 2, kModeCap = 3;
 
 struct DecodeLaunch {
   DecodeParams p;
@@ -222,10 +223,14 @@ inline size_t mq_smem_bytes(int32_t d, CacheKind cache, int32_t B, int32_t nc) {
 
 // Returns a CUDA error (cudaSuccess when the kernel was enqueued) or
 // cudaErrorNotSupported when no kernel is built for the combination.
-cudaError_t launch_decode_biased_f16(const DecodeLaunch& l);
-cudaError_t launch_decode_biased_bf16(const DecodeLaunch& l);
-cudaError_t launch_decode_biased_e4m3(const DecodeLaunch& l);
-cudaError_t launch_decode_biased_e4m3_tok(const DecodeLaunch& l);
+cudaError_t launch_decode_dist_f16(const DecodeLaunch& l);
+cudaError_t launch_decode_dist_bf16(const DecodeLaunch& l);
+cudaError_t launch_decode_dist_e4m3(const DecodeLaunch& l);
+cudaError_t launch_decode_dist_e4m3_tok(const DecodeLaunch& l);
+cudaError_t launch_decode_cap_f16(const DecodeLaunch& l);
+cudaError_t launch_decode_cap_bf16(const DecodeLaunch& l);
+cudaError_t launch_decode_cap_e4m3(const DecodeLaunch& l);
+cudaError_t launch_decode_cap_e4m3_tok(const DecodeLaunch& l);
 cudaError_t launch_decode_shared_f16(const DecodeLaunch& l);
 cudaError_t launch_decode_shared_bf16(const DecodeLaunch& l);
 cudaError_t launch_decode_f16(const DecodeLaunch& l);
@@ -318,13 +323,8 @@ struct PrefillLaunch {
 // What is done to the scores before the softmax.
 constexpr int kBiasCap = 1;   // cap tanh(s / cap)
 constexpr int kBiasDist = 2;  // + slope (key position - query position)
-constexpr int kBiasFine = 4;  // with kBiasCap: small scores under a wide cap keep every bit
-// Caps up to this keep the plain form of the tanh (pkv_device.cuh): its error,
-// 2^-22 of the cap in the score, is at most 2^-16, the weight's own rounding.
-constexpr float kCapCoarse = 64.f;
 cudaError_t launch_prefill(const PrefillLaunch& l);
 cudaError_t launch_prefill_cap(const PrefillLaunch& l);       // with or without slopes
-cudaError_t launch_prefill_cap_fine(const PrefillLaunch& l);  // with or without slopes
 cudaError_t launch_prefill_dist(const PrefillLaunch& l);
 
 // Attention over a prefix that a whole batch shares, over the sequences' own

@@ -79,8 +79,8 @@ struct Masked {
 };
 
 // BIAS: what is done to the scores before the softmax: kBiasCap caps them by a
-// tanh, kBiasDist adds a bias that grows with the distance (0: neither);
-// kBiasFine beside kBiasCap for caps above kCapCoarse.  A cap alone keeps the
+// tanh, kBiasDist adds a bias that grows with the distance (0: neither).  A cap
+// alone keeps the
 // order of the scores, so the max pass takes raw scores and caps their maximum;
 // with both, the max pass writes what the P pass needs back over the scores, so
 // that the tanh (four of the six special-function results of a pair) is
@@ -307,16 +307,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       return f2(slope2 * (float)(t0 - vis), slope2 * (float)(t0 + 1 - vis));
     };
     // two raw scores capped (log2 units), plus `add`
-    constexpr bool kFine = (BIAS & kBiasFine) != 0;
     auto cap_pair = [&](uint64_t raw, uint64_t add) -> uint64_t {
       const float2 z = f2_split(mul2(raw, cz2));
       const float2 u = f2_split(add2(f2(ex2(z.x), ex2(z.y)), f2(1.f, 1.f)));
-      const uint64_t r = f2(rcp(u.x), rcp(u.y));
-      if constexpr (!kFine) return fma2(r, mcap2, add2(cap2, add));
-      // a wide cap: near 0 by the series, which keeps every bit
-      const float2 f = f2_split(fma2(r, mcap2, cap2));
-      return add2(f2(cap_near_zero(z.x, p.cap_log2, f.x), cap_near_zero(z.y, p.cap_log2, f.y)),
-                  add);
+      return fma2(f2(rcp(u.x), rcp(u.y)), mcap2, add2(cap2, add));  // see cap_score
     };
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;

@@ -135,10 +135,9 @@ def attend(q, K, V, scale, t, cap=0.0, slopes=None, window=0, sinks=0):
         out[h] = (p[:, None] * v).sum(0) / p.sum()
         # Score error: d products summed in fp32, each addition cut (not
         # rounded) at 2^-23 of sums that stay below `size`; 2^-21 of the
-        # softmax exponent's range; 2^-21 of the cap; 20 roundings of the bias.
+        # cap (the tanh's 2^-22 and its scaling); 20 roundings of the bias.
         # A weight's own error: 2^-16 (its 16-bit pair), 2^-21 (exp2).
-        ds = size * d * 2.0 ** -23 + cap * 2.0 ** -21 * (1 if cap <= 64 else 0) \
-            + s.abs().max() * 2.0 ** -20 * (1 if cap > 64 else 0) + bias * 20 * 2.0 ** -24
+        ds = size * d * 2.0 ** -23 + cap * 2.0 ** -21 + bias * 20 * 2.0 ** -24
         tol[h] = v.abs().max() * 2 * (ds + 2.0 ** -15)
     return out, tol
 

@@ -42,7 +42,7 @@ DECODE = [  # Hq, Hkv, d, cache, cap, alibi, window, sinks, out, gain
     (4, 4, 128, "e4m3tok", 0.0, True, 200, 20, "f32", 1.0),
     (8, 2, 128, "bf16", 1000.0, False, 0, 0, "f32", 6.0),
     (8, 2, 128, "bf16", 2.0 ** -10, False, 0, 0, "f32", 6.0),
-    (8, 2, 128, "bf16", 2.0 ** 20, False, 0, 0, "f32", 1.0),
+    (8, 2, 128, "bf16", 2.0 ** 10, False, 0, 0, "f32", 1.0),
 ]
 
 
@@ -159,7 +159,7 @@ PREFILL = [  # Hq, Hkv, d, cache, lens, chunks, cap, alibi, out, gain
     (2, 1, 128, "bf16", [700, 16], [200, 5], 50.0, True, "bf16", 6.0),
     (4, 2, 64, "bf16", [260, 64], [130, 1], 300.0, False, "f32", 6.0),
     (4, 2, 64, "f16", [260, 64], [130, 1], 300.0, True, "f32", 6.0),
-    (4, 2, 128, "bf16", [150, 64], [100, 64], 2.0 ** 20, False, "f32", 1.0),
+    (4, 2, 128, "bf16", [150, 64], [100, 64], 2.0 ** 10, False, "f32", 1.0),
 ]
 
 
