@@ -796,6 +796,7 @@ pkv_status prefill_impl(const pkv_cache_desc* desc, const void* q, const void* k
   const cudaError_t e = softcap > 0.f       ? pkv::launch_prefill_cap(l)
                         : slopes != nullptr ? pkv::launch_prefill_dist(l)
                                             : pkv::launch_prefill(l);
+  if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 }  // namespace

@@ -90,9 +90,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmq,
                    const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv) {
-  const int b = blockIdx.x / p.tiles_per_seq;
-  const int ctile = blockIdx.x - b * p.tiles_per_seq;
-  const int h = blockIdx.y;                 // KV head
+  // The biased forms start the last rows of every sequence and head first: they
+  // see the longest stretch, and the short ones fill the end of the run.
+  int b, ctile, h;                          // sequence, pair of tiles, KV head
+  if constexpr (BIAS == 0) {
+    b = blockIdx.x / p.tiles_per_seq;
+    ctile = blockIdx.x - b * p.tiles_per_seq;
+    h = blockIdx.y;
+  } else {
+    const int rest = blockIdx.x / p.Hkv;
+    h = blockIdx.x - rest * p.Hkv;
+    ctile = p.tiles_per_seq - 1 - rest / p.B;
+    b = rest - rest / p.B * p.B;
+  }
   const int G = p.Hq / p.Hkv;               // query heads per KV head
   const int tpt = kPfRows / G;              // tokens per tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -569,7 +579,10 @@ cudaError_t launch_prefill_kernel(const PrefillLaunch& l) {
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(l.p.B * l.p.tiles_per_seq), (unsigned)l.p.Hkv, 1);
+  if (BIAS != 0 && (int64_t)l.p.B * l.p.tiles_per_seq * l.p.Hkv >= (int64_t)1 << 31)
+    return cudaErrorNotSupported;
+  cfg.gridDim = BIAS == 0 ? dim3((unsigned)(l.p.B * l.p.tiles_per_seq), (unsigned)l.p.Hkv, 1)
+                          : dim3((unsigned)(l.p.B * l.p.tiles_per_seq * l.p.Hkv), 1, 1);
   cfg.blockDim = dim3(kPfThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = l.stream;
