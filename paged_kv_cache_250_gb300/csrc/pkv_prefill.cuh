@@ -80,11 +80,12 @@ struct Masked {
 
 // BIAS: what is done to the scores before the softmax: kBiasCap caps them by a
 // tanh, kBiasDist adds a bias that grows with the distance (0: neither).  A cap
-// alone keeps the
-// order of the scores, so the max pass takes raw scores and caps their maximum;
-// with both, the max pass writes what the P pass needs back over the scores, so
-// that the tanh (four of the six special-function results of a pair) is
-// computed once.
+// alone keeps the order of the scores, so the max pass takes raw scores and caps
+// their maximum; with both, the max pass writes what the P pass needs back over
+// the scores, so that the tanh (four of the six special-function results of a
+// pair) is computed once: 12 sequences of up to 700 rows 208 us; with the tanh
+// computed in both passes 619, and in the max pass for one score of every four
+// (a reference at most 3 |slope| too high) 232.
 template <bool BF16, int D, int BIAS>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmq,

@@ -176,6 +176,20 @@ def test_prefill_matches_the_formula(case):
     assert torch.all(o[sum(chunks):] == 7.0)  # left as they were
 
 
+@pytest.mark.parametrize("cache", ["bf16", "f16"])
+@pytest.mark.parametrize("slopes", [(3.0, -4.0, 0.001, 40.0), (2.0, -2.0, 1.8, -1.8)])
+def test_prefill_cap_with_slopes_of_any_size(cache, slopes):
+    """Slopes so steep that a reference maximum a few tokens off would lose the
+    weights, of either sign, and just below that."""
+    p = Paged([300, 140, 37], 4, 2, 64, cache, 93)
+    chunks = [150, 140, 2]
+    q = p.queries(sum(chunks), 94, 3.0)
+    sl = torch.tensor(slopes)
+    o = prefill(p, q, chunks, "f32", 20.0, sl)
+    ref, tol = expect_prefill(p, q, chunks, 20.0, sl)
+    check(o, ref, tol, "f32", str(slopes))
+
+
 @pytest.mark.parametrize("cap,use_slopes", [(30.0, False), (0.0, True)])
 def test_prefill_long_sampled(cap, use_slopes):
     """600 rows behind 2500 cached tokens, sampled rows."""
