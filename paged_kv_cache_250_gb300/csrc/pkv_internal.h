@@ -323,6 +323,7 @@ struct PrefillLaunch {
 // What is done to the scores before the softmax.
 constexpr int kBiasCap = 1;   // cap tanh(s / cap)
 constexpr int kBiasDist = 2;  // + slope (key position - query position)
+size_t prefill_smem_bytes(int d);
 cudaError_t launch_prefill(const PrefillLaunch& l);
 cudaError_t launch_prefill_cap(const PrefillLaunch& l);       // with or without slopes
 cudaError_t launch_prefill_dist(const PrefillLaunch& l);

@@ -1,8 +1,6 @@
 // Paged prefill attention with a distance bias.
-#include "pkv_prefill.cuh"
+#include "pkv_prefill_biased.cuh"
 
 namespace pkv {
-cudaError_t launch_prefill_dist(const PrefillLaunch& l) {
-  return pf::launch_prefill_bias<kBiasDist>(l);
-}
+cudaError_t launch_prefill_dist(const PrefillLaunch& l) { return pfb::launch_bias<kBiasDist>(l); }
 }  // namespace pkv
