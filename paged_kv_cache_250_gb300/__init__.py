@@ -215,19 +215,6 @@ def _on(t: Optional[torch.Tensor], dev: int, name: str) -> Optional[int]:
     return t.data_ptr()
 
 
-def _rows_on(t: torch.Tensor, dev: int, name: str, T: int, H: int, d: int):
-    """Device address and token stride of a [T][H][d] tensor on device dev whose
-    tokens may lie apart (a part of a fused projection)."""
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor, on the device of q")
-    if t.shape != (T, H, d):
-        raise ValueError(f"{name} must be [tokens][heads][d], with the cache's heads and d")
-    st, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and H > 1):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.data_ptr(), st if T > 1 else H * d
-
-
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
@@ -308,27 +295,33 @@ def pkv_kv_append_rope(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Te
         with torch.cuda.device(dev):
             return pkv_kv_append_rope(desc, k_cache, v_cache, slot_mapping, positions, cos_sin, q,
                                       k, v, q_out, interleaved, stream)
-    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
+    i64 = torch.int64
+    if slot_mapping.dtype is not i64 or positions.dtype is not i64:
         raise ValueError("slot_mapping and positions must be int64")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be fp32 [max_position][rot_dim]")
     dt = q.dtype
-    if k.dtype != dt or v.dtype != dt or q_out.dtype != dt:
+    if k.dtype is not dt or v.dtype is not dt or q_out.dtype is not dt:
         raise ValueError("q, k, v and q_out must have one type")
     T, Hq, Hkv, d = slot_mapping.numel(), desc.num_q_heads, desc.num_kv_heads, desc.head_dim
     if positions.numel() != T:
         raise ValueError("slot_mapping and positions need one entry per token")
-    if q_out.shape != (T, Hq, d):
-        raise ValueError("q_out must be [T][Hq][d]")
-    qp, qs = _rows_on(q, dev, "q", T, Hq, d)
-    kp, ks = _rows_on(k, dev, "k", T, Hkv, d)
-    vp, vs = _rows_on(v, dev, "v", T, Hkv, d)
+    qshape, kvshape = (T, Hq, d), (T, Hkv, d)
+    if q.shape != qshape or q_out.shape != qshape or k.shape != kvshape or v.shape != kvshape:
+        raise ValueError("q and q_out must be [T][Hq][d], k and v [T][Hkv][d]")
+    (qs, qh, qd), (ks, kh, kd), (vs, vh, vd) = q.stride(), k.stride(), v.stride()
+    if not (qd == kd == vd == 1 and (qh == d or Hq == 1) and (kh == vh == d or Hkv == 1)):
+        raise ValueError("the heads of a token of q, k and v must be contiguous")
+    if T == 1:  # the stride of a single row says nothing
+        qs, ks, vs = Hq * d, Hkv * d, Hkv * d
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("k and v must be on the device of q")
     max_pos, rot = cos_sin.shape
     st = lib.pkv_kv_append_rope(
         ctypes.byref(desc), _on(k_cache, dev, "k_cache"), _on(v_cache, dev, "v_cache"),
         _on(slot_mapping, dev, "slot_mapping"), _on(positions, dev, "positions"),
-        _on(cos_sin, dev, "cos_sin"), max_pos, rot, qp, qs, kp, ks, vp, vs,
-        _on(q_out, dev, "q_out"), T, _DTYPE_CODE.get(dt, -1),
+        _on(cos_sin, dev, "cos_sin"), max_pos, rot, q.data_ptr(), qs, k.data_ptr(), ks,
+        v.data_ptr(), vs, _on(q_out, dev, "q_out"), T, _DTYPE_CODE.get(dt, -1),
         PKV_ROPE_INTERLEAVED if interleaved else 0, _stream_on(stream, dev))
     if st:
         raise PkvError(st, "pkv_kv_append_rope")
