@@ -148,8 +148,8 @@ __device__ __forceinline__ void store_out_rt(pkv_dtype t, void* base, int64_t id
 // branch: with the two behind uniform branches, which keep a page's MMAs and the
 // next one's scores apart, 64 sequences of up to 8192 tokens in an E4M3 cache
 // under a window of 4096 took 116.6 us, now 109.7 with both, 105.2 with the bias
-// alone (the plain kernel: 99.8); kModeShared reads a prefix that all sequences share through its
-// own table.
+// alone (the plain kernel: 99.8).  kModeShared reads a prefix that all sequences
+// share through its own table.
 template <int D, int G, int QC, int CACHE, bool QBF16, bool DEEP, int MODE>
 __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCtasPerSm)
     decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,

@@ -153,7 +153,7 @@ struct DecodeParams {
   int32_t npb;
 };
 // Forms of the single-token kernel: distance bias alone, cap (with a distance
-// bias of zero slope or more), shared prefix.
+// bias, of slope zero where none is given), shared prefix.
 constexpr int kModePlain = 0, kModeDist = 1, kModeShared = 2, kModeCap = 3;
 
 struct DecodeLaunch {

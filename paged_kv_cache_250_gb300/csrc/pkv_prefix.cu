@@ -25,15 +25,27 @@
 //   P           hi + lo 16-bit pairs over S in tensor memory (the weights keep
 //               about 16 bits, as in the framework's other attention kernels);
 //   O += P V    tcgen05.mma with A from tensor memory, twice per 16 tokens.
+// Bound by the softmax and the products taking turns on each stream.  256
+// sequences behind 32768 tokens, 32/8 heads of 128: 8192 units in about 165 us,
+// 0.83 PFLOP/s (1.25 with the second product of P).  Equal shares replaced a grid
+// of (pair, head, split) with the splits picked by a search, which took 299 us
+// for the whole call (now 215).  Measured and not kept: steps
+// of 64 tokens with two score buffers, as in the biased prefill kernel (211 to
+// 240 us; an MMA of N 64 takes as long as one of N 128), more registers for the
+// softmax warps by setmaxnreg (180 us), MMAs issued by a converged warp (187).
 //
 // own_kernel.  One warp per CTA and per chunk of one sequence's own pages of
 // one KV head: the page ring, MMAs and softmax of the single-token decode
-// kernel's warp, with nothing to hand over at a segment's end.  It depends on
+// kernel's warp, with nothing to hand over at a segment's end; bound by HBM
+// (269 MB of own pages, 256 sequences of 256 tokens: about 45 us; the decode
+// kernel's form, which leaves a partial per share, took 127).  It depends on
 // nothing the prefix kernel writes and needs little of an SM (a 24 KB ring), so
-// it is launched to run beside it: the prefix is bound by the tensor cores and
-// its softmax, the own parts by HBM.
+// its first CTAs start beside the prefix kernel's and the rest as SMs come
+// free.  All of it beside the prefix kernel, from a queue, was slower: the
+// prefix then took 270 us and the call 301 (227 at the time).
 //
-// prefix_merge_kernel.  A warp per row adds the parts in a fixed order.
+// prefix_merge_kernel.  A warp per row adds the parts in a fixed order (5 us of
+// the same call).
 #include <atomic>
 
 #include "pkv_device.cuh"
@@ -93,7 +105,8 @@ struct Line {
   __device__ int64_t start(int pair, int h) const {
     return (int64_t)Hkv * nblk * 2 * pair + (int64_t)h * nblk * weight(pair);
   }
-  __device__ int64_t share(int64_t c) const { return udiv64(c * cost + n - 1, n); }  // first cost of CTA c
+  // first cost of CTA c
+  __device__ int64_t share(int64_t c) const { return udiv64(c * cost + n - 1, n); }
   __device__ int64_t cta_of(int64_t x) const { return udiv64(x * n, cost); }
 };
 // One CTA's blocks of one segment.
@@ -143,10 +156,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* max_len = reinterpret_cast<int32_t*>(base_ptr + kOffMisc + 8);
   volatile int32_t* armed = reinterpret_cast<volatile int32_t*>(base_ptr + kOffMisc + 12);
 
-  if (warp == 0) {
-    tmem_alloc(base + kOffMisc, kTmemCols);
-    tmem_relinquish();
-  }
   if (tid == 0) {
     prefetch_tmap(&tmq);
     prefetch_tmap(&tmk);
@@ -159,16 +168,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   // so far nothing of the kernel in front was needed, and it may still run
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the kernel behind this one reads nothing that this one writes before its
   // own end, and everything earlier is complete: it may start
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Tensor memory is taken behind the wait, never before it: a kernel in front
+  // that lets this one start may have yet to take its own on the same SM.
+  if (warp == 0) {
+    tmem_alloc(base + kOffMisc, kTmemCols);
+    tmem_relinquish();
+  }
 
   // the positions any sequence sees of the prefix: rows of V behind them may
   // never have been written
@@ -178,7 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0 && m > 0) atomicMax(max_len, m);
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   const int seen = *max_len;
   if (blockIdx.x == 0 && tid == 0) *p.seen = seen;  // for the merge
   const Line line(p, seen);
@@ -304,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(kBarSFull + t);
         if (last) commit(kBarKFree + bb);
       };
-      auto pv = [&](int t, int bb, bool add, bool last) {  // P_t: per 64 tokens 32 columns of hi, then 32 of lo pairs
+      // P_t: per 64 tokens 32 columns of hi pairs, then 32 of lo pairs
+      auto pv = [&](int t, int bb, bool add, bool last) {
         const uint64_t b0 = dv + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
         const uint32_t pt = tmem + (uint32_t)t * kTok;
         const uint32_t dt = tmem + 256 + (uint32_t)t * D;
@@ -998,8 +1014,9 @@ cudaError_t launch(const PrefixLaunch& l) {
   // a warp per row where rows are many and their parts few
   const int64_t segs = (int64_t)l.p.pairs * l.p.Hkv;
   if (rows >= kMergeRows && l.p.ctas < kMergeParts * segs)
-    return launch_behind(prefix_merge_kernel<D, 1>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps),
-                         kMergeWarps * 32, 0, l.stream, l.p);
+    return launch_behind(prefix_merge_kernel<D, 1>,
+                         (unsigned)((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0,
+                         l.stream, l.p);
   return launch_behind(prefix_merge_kernel<D, kMergeWarps>, (unsigned)rows, kMergeWarps * 32, 0,
                        l.stream, l.p);
 }
