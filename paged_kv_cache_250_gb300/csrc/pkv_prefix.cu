@@ -26,26 +26,29 @@
 //               about 16 bits, as in the framework's other attention kernels);
 //   O += P V    tcgen05.mma with A from tensor memory, twice per 16 tokens.
 // Bound by the softmax and the products taking turns on each stream.  256
-// sequences behind 32768 tokens, 32/8 heads of 128: 8192 units in about 165 us,
-// 0.83 PFLOP/s (1.25 with the second product of P).  Equal shares replaced a grid
-// of (pair, head, split) with the splits picked by a search, which took 299 us
-// for the whole call (now 215).  Measured and not kept: steps
-// of 64 tokens with two score buffers, as in the biased prefill kernel (211 to
-// 240 us; an MMA of N 64 takes as long as one of N 128), more registers for the
-// softmax warps by setmaxnreg (180 us), MMAs issued by a converged warp (187).
+// sequences behind 32768 tokens, 32/8 heads of 128: 8192 units in 167 us, 0.82
+// PFLOP/s (1.24 with the second product of P).  Equal shares replaced a grid of
+// (pair, head, split) with the splits picked by a search, which took 299 us for
+// the whole call (227 at that step, now 215).  Measured and not kept: steps of
+// 64 tokens with two score buffers, as in the biased prefill kernel (211 to 240
+// us, 176 at the time; an MMA of N 64 takes as long as one of N 128), more
+// registers for the softmax warps by setmaxnreg (180), MMAs issued by a
+// converged warp (187).
 //
 // own_kernel.  One warp per CTA and per chunk of one sequence's own pages of
 // one KV head: the page ring, MMAs and softmax of the single-token decode
 // kernel's warp, with nothing to hand over at a segment's end; bound by HBM
-// (269 MB of own pages, 256 sequences of 256 tokens: about 45 us; the decode
-// kernel's form, which leaves a partial per share, took 127).  It depends on
+// (269 MB of own pages, 256 sequences of up to 512 tokens: 49 us alone and cold,
+// 5.5 TB/s; the decode kernel's form, which leaves a partial per share, took
+// 127).  It depends on
 // nothing the prefix kernel writes and needs little of an SM (a 24 KB ring), so
 // its first CTAs start beside the prefix kernel's and the rest as SMs come
 // free.  All of it beside the prefix kernel, from a queue, was slower: the
 // prefix then took 270 us and the call 301 (227 at the time).
 //
-// prefix_merge_kernel.  A warp per row adds the parts in a fixed order (5 us of
-// the same call).
+// prefix_merge_kernel.  A warp per row adds the parts in a fixed order, four
+// warps where rows are few and their parts many; bound by the latency of the
+// parts, which are in L2 (16 us alone and cold, about 5 in the same call).
 #include <atomic>
 
 #include "pkv_device.cuh"
