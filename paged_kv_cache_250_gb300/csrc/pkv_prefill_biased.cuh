@@ -116,7 +116,7 @@ __device__ __forceinline__ void teardown(const Cta& c, int32_t* err_word) {
     if (i == 0) report_error(err_word, PKV_ERR_TIMEOUT);
     if (i < kBarKFree && c.armed[i] > 0)
       mbar_wait_bounded(c.bar(i), (uint32_t)((c.armed[i] - 1) & 1), kWaitNs);
-    if (i == 8 * 32) {  // the thread that issued the MMAs
+    if (i >> 5 == 8 && elect_one()) {  // the thread that issued the MMAs
       umma_commit(c.bar(kBarDrain));
       mbar_wait_bounded(c.bar(kBarDrain), 0, kWaitNs);
     }
@@ -177,23 +177,20 @@ __device__ __forceinline__ void copy_steps(const Cta& c, int N, const void* tmk,
   }
 }
 
-// The MMA warp.  All lanes go through the loop and lane 0 issues: control flow
-// and descriptors are then uniform over the warp, and an issue costs no moves of
-// its operands into uniform registers (1439 us where the loop ran in one lane).
+// The MMA warp's elected lane.
 template <bool BF16, int D>
 __device__ __forceinline__ void mma_steps(const Cta& c, int N) {
   using PL = Plan<D>;
   constexpr int NH = PL::NH;
   constexpr uint32_t kIdS = idesc_f16(BF16, false, kRows, kTok);
   constexpr uint32_t kIdO = idesc_f16(BF16, true, kRows, D);
-  const uint32_t lead = (threadIdx.x & 31) == 0;
   const uint64_t dq = sdesc(c.base, 16, 1024);
   const uint64_t dk = sdesc(c.base + PL::kOffK, 16, 1024);
   const uint64_t dv = sdesc(c.base + PL::kOffV, kSHalf, 1024);
   auto qk = [&](int t, int i) -> bool {  // scores of tile t's step i
     const uint32_t s = (uint32_t)i & (kSlots - 1), sb = (uint32_t)i & 1;
     if (t == 0) {
-      if (!c.wait_warp(kBarKFull + (int)s, ((uint32_t)i / kSlots) & 1)) return false;
+      if (!c.wait(kBarKFull + (int)s, ((uint32_t)i / kSlots) & 1)) return false;
       tc_fence_after();
     }
     const uint64_t a0 = dq + (t ? (uint64_t)NH * kQHalf >> 4 : 0ull);
@@ -202,17 +199,17 @@ __device__ __forceinline__ void mma_steps(const Cta& c, int N) {
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       const uint32_t in = (uint32_t)(ks & 3) * 32;
-      umma_if(lead, d0, a0 + (((uint32_t)(ks >> 2) * kQHalf + in) >> 4),
-              b0 + (((uint32_t)(ks >> 2) * kSHalf + in) >> 4), kIdS, ks > 0);
+      umma(d0, a0 + (((uint32_t)(ks >> 2) * kQHalf + in) >> 4),
+           b0 + (((uint32_t)(ks >> 2) * kSHalf + in) >> 4), kIdS, ks > 0);
     }
-    umma_commit_if(lead, c.bar(kBarSFull + 2 * t + (int)sb));
-    if (t == 1) umma_commit_if(lead, c.bar(kBarKFree + (int)s));
+    umma_commit(c.bar(kBarSFull + 2 * t + (int)sb));
+    if (t == 1) umma_commit(c.bar(kBarKFree + (int)s));
     return true;
   };
   auto pv = [&](int t, int i) -> bool {
     const uint32_t s = (uint32_t)i & (kSlots - 1), sb = (uint32_t)i & 1;
-    if (!c.wait_warp(kBarPFull + 2 * t + (int)sb, ((uint32_t)i >> 1) & 1)) return false;
-    if (t == 0 && !c.wait_warp(kBarVFull + (int)s, ((uint32_t)i / kSlots) & 1)) return false;
+    if (!c.wait(kBarPFull + 2 * t + (int)sb, ((uint32_t)i >> 1) & 1)) return false;
+    if (t == 0 && !c.wait(kBarVFull + (int)s, ((uint32_t)i / kSlots) & 1)) return false;
     tc_fence_after();
     const uint64_t b0 = dv + ((uint64_t)s * NH * kSHalf >> 4);
     const uint32_t pt = c.tmem + (uint32_t)t * 128 + sb * kTok;  // 32 columns of hi, 32 of lo
@@ -220,14 +217,14 @@ __device__ __forceinline__ void mma_steps(const Cta& c, int N) {
 #pragma unroll
     for (int ks = 0; ks < kTok / 16; ++ks) {
       const uint64_t bv = b0 + ((uint32_t)ks * 16 * 128 >> 4);
-      umma_ts_if(lead, dt, pt + (uint32_t)ks * 8, bv, kIdO, i > 0 || ks > 0);
-      umma_ts_if(lead, dt, pt + 32 + (uint32_t)ks * 8, bv, kIdO, 1);
+      umma_ts(dt, pt + (uint32_t)ks * 8, bv, kIdO, i > 0 || ks > 0);
+      umma_ts(dt, pt + 32 + (uint32_t)ks * 8, bv, kIdO, 1);
     }
-    umma_commit_if(lead, c.bar(kBarODone + 2 * t + (int)sb));
-    if (t == 1) umma_commit_if(lead, c.bar(kBarVFree + (int)s));
+    umma_commit(c.bar(kBarODone + 2 * t + (int)sb));
+    if (t == 1) umma_commit(c.bar(kBarVFree + (int)s));
     return true;
   };
-  if (!c.wait_warp(kBarQ, 0)) return;
+  if (!c.wait(kBarQ, 0)) return;
   for (int i = 0; i < min(N, 2); ++i) {
     if (!qk(0, i) || !qk(1, i)) return;
   }
@@ -459,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     copy_steps<D>(c, N, &tmk, &tmv, p.block_tables + (int64_t)b * p.MBS,
                   (ctx + kPageSize - 1) / kPageSize, h, p.Hkv, p.NB, p.err_word);
   } else if (warp == 8) {
-    mma_steps<BF16, D>(c, N);
+    if (elect_one()) mma_steps<BF16, D>(c, N);
   } else {
     const int t = warp >> 2, tt = tid - t * kRows;
     const int row = tok_base + t * tpt + tt / G;  // new token of this row

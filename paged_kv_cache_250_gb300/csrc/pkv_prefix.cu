@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kIdS = idesc_f16(BF16, false, kRows, kTok);
       constexpr uint32_t kIdO = idesc_f16(BF16, true, kRows, D);
       auto commit = [&](int i) {
