@@ -17,10 +17,13 @@
 // when the softmax of step i ends: a tile's softmax runs without a break, and
 // waits for its products only to rescale O, which it seldom does.
 // Four sequences of 2048 rows behind 6144 tokens, 32/8 heads of 128, capped:
-// 1390 us, against 1488 with the prefill kernel's steps of 128 tokens and one
-// buffer, where a tile's softmax and its products take turns; 12 sequences of up
-// to 700 rows with cap and slopes 193 against 208.  The steps' 32 MMAs, about 90
-// cycles each (N 64 costs no less than N 128), now set the pace.
+// 1399 us, against 1488 with the prefill kernel's steps of 128 tokens and one
+// buffer, where a tile's softmax and its products take turns; 1370 with the MMAs
+// issued behind elect.sync.  12 sequences of up to 700 rows with cap and slopes:
+// 187, before 208.  A step takes about 3500 cycles, of which its 32 MMAs are 1790
+// (N 64: 48 each, N 128: 64) and the special-function unit's work for the two
+// softmax warps of a scheduler about 2050; the latency of those two warps (issue
+// 43 %) is what is left, and their registers leave no room for more.
 #pragma once
 
 #include <atomic>
@@ -67,6 +70,7 @@ struct Cta {
   // A bounded wait; one that gives up raises the CTA's abort flag, after which
   // no role waits any more.
   __device__ bool wait(int i, uint32_t parity) const {
+    if (mbar_try_wait(bar(i), parity)) return true;
     if (*abort_flag) return false;
     if (mbar_wait_bounded(bar(i), parity, kWaitNs)) return true;
     *abort_flag = 1;
@@ -394,10 +398,10 @@ __device__ __forceinline__ bool softmax_steps(const Cta& c, int N, int t, int tt
                             (uint32_t)(ch & 7) * 16;
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ad), "r"(0) : "memory");
       }
+      // the tensor cores read them through the async proxy
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     tmem_st_wait();
-    // zeroed V rows are read by the tensor cores (async proxy)
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar(kBarPFull + 2 * t + (int)sb));

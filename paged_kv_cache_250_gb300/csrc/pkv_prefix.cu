@@ -26,14 +26,14 @@
 //               about 16 bits, as in the framework's other attention kernels);
 //   O += P V    tcgen05.mma with A from tensor memory, twice per 16 tokens.
 // Bound by the softmax and the products taking turns on each stream.  256
-// sequences behind 32768 tokens, 32/8 heads of 128: 8192 units in 167 us, 0.82
-// PFLOP/s (1.24 with the second product of P).  Equal shares replaced a grid of
-// (pair, head, split) with the splits picked by a search, which took 299 us for
-// the whole call (227 at that step, now 215).  Measured and not kept: steps of
-// 64 tokens with two score buffers, as in the biased prefill kernel (211 to 240
-// us, 176 at the time; an MMA of N 64 takes as long as one of N 128), more
-// registers for the softmax warps by setmaxnreg (180), MMAs issued by a
-// converged warp (187).
+// sequences behind 32768 tokens, 32/8 heads of 128: 8192 units in 149 us, 0.92
+// PFLOP/s (1.38 with the second product of P); 167 us before the MMAs were issued
+// behind elect.sync.  Equal shares replaced a grid of (pair, head, split) with
+// the splits picked by a search, which took 299 us for the whole call (227 at
+// that step, now 194).  Measured and not kept: steps of 64 tokens with two score
+// buffers, as in the biased prefill kernel (193 us for the call against 195: the
+// softmax warps' latency bounds both), more registers for the softmax warps by
+// setmaxnreg (180, 176 at the time).
 //
 // own_kernel.  One warp per CTA and per chunk of one sequence's own pages of
 // one KV head: the page ring, MMAs and softmax of the single-token decode
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t at = lo;
 
   auto wait = [&](int i, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar(i), parity)) return true;
     if (*abort_flag) return false;
     if (mbar_wait_bounded(bar(i), parity, kWaitNs)) return true;
     *abort_flag = 1;
@@ -547,8 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                              (uint32_t)(ch & 7) * 16;
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
         }
+        // the tensor cores read them through the async proxy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarPFull + t));
