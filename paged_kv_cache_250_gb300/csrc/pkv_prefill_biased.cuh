@@ -20,7 +20,7 @@
 // 1399 us, against 1488 with the prefill kernel's steps of 128 tokens and one
 // buffer, where a tile's softmax and its products take turns; 1370 with the MMAs
 // issued behind elect.sync.  12 sequences of up to 700 rows with cap and slopes:
-// 187, before 208.  A step takes about 3500 cycles, of which its 32 MMAs are 1790
+// 189, before 208.  A step takes about 3500 cycles, of which its 32 MMAs are 1790
 // (N 64: 48 each, N 128: 64) and the special-function unit's work for the two
 // softmax warps of a scheduler about 2050; the latency of those two warps (issue
 // 43 %) is what is left.  Twice the warps, two groups per tile that take the steps
