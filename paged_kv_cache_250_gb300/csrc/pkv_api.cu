@@ -11,6 +11,7 @@
 
 #include "pkv.h"
 #include "pkv_internal.h"
+#include "pkv_prefix_line.h"
 
 namespace {
 
@@ -217,7 +218,7 @@ SharedLayout shared_layout(const pkv_cache_desc* d, int32_t batch, int sms) {
   const int64_t g = d->num_q_heads / d->num_kv_heads;
   const int64_t segs = (int64_t)batch * d->num_kv_heads;
   SharedLayout s;
-  s.pairs = (int32_t)(((int64_t)batch * g + 255) / 256);
+  s.pairs = pkv::prefix_pairs((int64_t)batch * g);
   const int64_t pre_rows = ((int64_t)sms + (int64_t)s.pairs * d->num_kv_heads) * 256;
   const int64_t own_rows = (segs > kOwnItems ? segs : kOwnItems) * g;
   s.pre_ml = 256;
@@ -711,7 +712,12 @@ pkv_status pkv_paged_decode_attention_shared_prefix(
   l.p.MBS = max_blocks_per_seq;
   l.p.npb = num_prefix_blocks;
   l.p.pairs = s.pairs;
-  l.p.ctas = sms;
+  const int64_t blocks = pkv::prefix_blocks_of((int64_t)num_prefix_blocks * kPageSize);
+  const int64_t rows = (int64_t)batch * (desc->num_q_heads / desc->num_kv_heads);
+  const int last_w = pkv::prefix_last_weight(rows, s.pairs);
+  l.p.ctas = (int32_t)pkv::prefix_ctas(
+      pkv::prefix_cost(desc->num_kv_heads, blocks, s.pairs, last_w), sms);
+  l.sms = sms;
   // own parts are cut into chunks of kOwnPages pages or more, about kOwnItems in
   // all (from the longest own part the arguments allow: empty chunks are cheap)
   const int64_t cap = (int64_t)max_blocks_per_seq * kPageSize;

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "pkv.h"
+#include "pkv_hd.h"
 
 namespace pkv {
 
@@ -97,13 +98,6 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
   return pol;
-}
-
-// a / b for a >= 0, b > 0: a 32-bit division when both fit (the usual case;
-// a 64-bit division is a long instruction sequence)
-__device__ __forceinline__ int64_t udiv64(int64_t a, int64_t b) {
-  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-  return a / b;
 }
 
 // Pull `bytes` (a multiple of 16, 16-byte aligned) at `src` into L2; no data

@@ -347,7 +347,7 @@ struct PrefixParams {
   int32_t* err_word;
   int32_t B, Hq, Hkv, NB, MBS, npb;
   int32_t pairs;                 // pairs of 128-row tiles of the B g rows of a KV head
-  int32_t ctas;                  // of the prefix kernel, at most
+  int32_t ctas;                  // of the prefix kernel, as launched
   int32_t chunks, chunk_pages;   // of an own part
   pkv_dtype out_dtype;
   float scale_log2;
@@ -357,23 +357,11 @@ struct PrefixLaunch {
   CUtensorMap tmap_q;  // [B][Hq][d], boxes of 128 / g sequences x g heads x 64
   CUtensorMap tmap_k;
   CUtensorMap tmap_v;
+  int32_t sms;
   bool bf16;
   int32_t d;
   cudaStream_t stream;
 };
-// CTAs of the prefix kernel with work.  In units of a block of 128 tokens of a
-// pair of row tiles (cost 2; 1 where the second tile is empty, two of which run
-// side by side) the longest share is m = ceil(units / ctas); while m is small,
-// as many CTAs as shares of m take, no more: fewer partials in the same time
-// (64 sequences behind 8192 tokens, m = 4: 128 CTAs 41.1 us, 152 43.2).  A share
-// is at least one unit, so every CTA between a segment's first and last has a
-// part of it.
-__host__ __device__ inline int64_t prefix_ctas(int64_t cost, int32_t ctas) {
-  const int64_t units = cost >> 1 > 0 ? cost >> 1 : 1;
-  for (int m = 1; m <= 4; ++m)
-    if (units <= (int64_t)m * ctas) return ((uint32_t)units + m - 1) / m;
-  return ctas;
-}
 cudaError_t launch_prefix(const PrefixLaunch& l);  // the three kernels
 
 }  // namespace pkv

@@ -53,12 +53,13 @@
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_prefix_line.h"
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace px {
 
-constexpr int kRows = 128, kTok = 128;  // rows of a tile, cached tokens of a block
+constexpr int kRows = kPrefixRows, kTok = kPrefixTok;
 constexpr int kPages = kTok / kPageSize;
 constexpr int kThreads = 320;
 constexpr uint32_t kHalf = 16384;  // 128 rows x 128 bytes: 64 d columns of a tile or block
@@ -93,48 +94,9 @@ __device__ __forceinline__ int prefix_len(int c, const PrefixParams& p) {
   return c < 0 || c > p.MBS * kPageSize ? 0 : min(c, p.npb * kPageSize);
 }
 
-// The line of units: pair-major, then KV head, then block.  A block of a pair
-// costs w = 2, or 1 where the second tile is empty (only in the last pair).
-struct Line {
-  int Hkv, pairs, nblk, last_w;
-  int64_t cost, n;  // whole cost; CTAs with work
-  __device__ Line(const PrefixParams& p, int seen)
-      : Hkv(p.Hkv), pairs(p.pairs), nblk((seen + kTok - 1) / kTok) {
-    last_w = (2 * pairs - 1) * kRows < p.B * (p.Hq / p.Hkv) ? 2 : 1;
-    cost = (int64_t)Hkv * nblk * (2 * (pairs - 1) + last_w);
-    n = prefix_ctas(cost, p.ctas);
-  }
-  __device__ int weight(int pair) const { return pair == pairs - 1 ? last_w : 2; }
-  __device__ int64_t start(int pair, int h) const {
-    return (int64_t)Hkv * nblk * 2 * pair + (int64_t)h * nblk * weight(pair);
-  }
-  // first cost of CTA c
-  __device__ int64_t share(int64_t c) const { return udiv64(c * cost + n - 1, n); }
-  __device__ int64_t cta_of(int64_t x) const { return udiv64(x * n, cost); }
-};
-// One CTA's blocks of one segment.
-struct Part {
-  int pair, h, j0, nblk;
-  bool two;
-};
-// Steps through the segments that the costs [x, hi) cross; false at the end.
-// A unit belongs to the share its first cost lies in.
-__device__ __forceinline__ bool next_part(const Line& ln, int64_t& x, int64_t hi, Part& s) {
-  while (x < hi) {
-    const int64_t per = (int64_t)ln.Hkv * ln.nblk * 2;
-    s.pair = ln.pairs == 1 ? 0 : (int)min(udiv64(x, per), (int64_t)(ln.pairs - 1));
-    const int w = ln.weight(s.pair);
-    s.two = w == 2;
-    const int64_t seg = (int64_t)ln.nblk * w;
-    s.h = (int)udiv64(x - per * s.pair, seg);
-    const int64_t s0 = ln.start(s.pair, s.h);
-    s.j0 = (int)((x - s0 + w - 1) >> (w - 1));  // w is 1 or 2
-    const int64_t j1 = min((int64_t)ln.nblk, (hi - s0 + w - 1) >> (w - 1));
-    s.nblk = (int)(j1 - s.j0);
-    x = s0 + seg;
-    if (s.nblk > 0) return true;
-  }
-  return false;
+// What is seen of the prefix, cut over the CTAs that were launched.
+__device__ __forceinline__ PrefixLine line_of(const PrefixParams& p, int seen) {
+  return PrefixLine(p.Hkv, (int64_t)p.B * (p.Hq / p.Hkv), p.pairs, seen, p.ctas);
 }
 
 template <bool BF16, int D>
@@ -199,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int seen = *max_len;
   if (blockIdx.x == 0 && tid == 0) *p.seen = seen;  // for the merge
-  const Line line(p, seen);
+  const PrefixLine line = line_of(p, seen);
   const int64_t lo = blockIdx.x < line.n && seen > 0 ? line.share(blockIdx.x) : 0;
   const int64_t hi = blockIdx.x < line.n && seen > 0 ? line.share(blockIdx.x + 1) : 0;
 
@@ -208,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of the buffers and the streams run on from part to part (they give the
   // barriers' phases).
   struct Walk {
-    Part s;
+    PrefixPart s;
     int buf0 = 0, buf1 = 0, str0 = 0, str1 = 0;  // uses before this part
     __device__ int count(int t) const { return s.two ? s.nblk : (s.nblk + 1 - t) / 2; }
     __device__ int block(int t, int i) const { return s.j0 + (s.two ? i : 2 * i + t); }
@@ -559,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && nt > 0)
       ok = __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + nt - 1) & 1)));
     if (!ok) break;
-    const int64_t slot = ((int64_t)blockIdx.x + wk.s.pair * p.Hkv + wk.s.h) * 2 + t;
+    const int64_t slot = line.slot(blockIdx.x, wk.s.pair, wk.s.h) * 2 + t;
     const bool any = nt > 0 && l_sum != 0.f;  // NaN counts: it has to show
     if (b < p.B) p.pre_ml[slot * kRows + tt] = any ? make_float2(m_ref, l_sum)
                                                    : make_float2(-INFINITY, 0.f);
@@ -886,13 +848,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
     int npre = 0, streams = 1;
     int64_t pre0 = 0;
     if (seen > 0) {
-      const Line line(p, seen);
-      const int w = line.weight(pair);
-      const int64_t s0 = line.start(pair, h);
-      const int64_t c0 = line.cta_of(s0), c1 = line.cta_of(s0 + (int64_t)(line.nblk - 1) * w);
-      streams = w == 2 ? 1 : 2;
+      const PrefixLine line = line_of(p, seen);
+      const bool two = line.weight(pair) == 2;
+      const int64_t c0 = line.first_cta(pair, h), c1 = line.last_cta(pair, h);
+      streams = two ? 1 : 2;
       npre = (int)(c1 - c0 + 1) * streams;
-      pre0 = (c0 + pair * p.Hkv + h) * 2 + (w == 2 ? tile & 1 : 0);
+      pre0 = line.slot(c0, pair, h) * 2 + (two ? tile & 1 : 0);
     }
     const int ctx = p.context_lens[b];
     const int own = ctx < 0 || ctx > p.MBS * kPageSize
@@ -1006,11 +967,8 @@ cudaError_t launch(const PrefixLaunch& l) {
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   static_assert(OwnPlan<D>::kSmem <= 48 * 1024, "no attribute needed");
-  const int64_t nblk = ((int64_t)l.p.npb * kPageSize + kTok - 1) / kTok;
-  const int last_w = (2 * l.p.pairs - 1) * kRows < l.p.B * G ? 2 : 1;
-  const int64_t cost = l.p.Hkv * nblk * (2 * (l.p.pairs - 1) + last_w);
-  e = launch_behind(pre, (unsigned)prefix_ctas(cost, l.p.ctas), kThreads, Plan<D>::kSmem, l.stream,
-                    l.p, l.tmap_q, l.tmap_k, l.tmap_v);
+  e = launch_behind(pre, (unsigned)l.p.ctas, kThreads, Plan<D>::kSmem, l.stream, l.p, l.tmap_q,
+                    l.tmap_k, l.tmap_v);
   if (e != cudaSuccess) return e;
   e = launch_behind(own, (unsigned)((int64_t)l.p.B * l.p.Hkv * l.p.chunks), 32, OwnPlan<D>::kSmem,
                     l.stream, l.p, l.tmap_k, l.tmap_v);
@@ -1018,7 +976,7 @@ cudaError_t launch(const PrefixLaunch& l) {
   const int64_t rows = (int64_t)l.p.B * l.p.Hq;
   // a warp per row where rows are many and their parts few
   const int64_t segs = (int64_t)l.p.pairs * l.p.Hkv;
-  if (rows >= kMergeRows && l.p.ctas < kMergeParts * segs)
+  if (rows >= kMergeRows && l.sms < kMergeParts * segs)
     return launch_behind(prefix_merge_kernel<D, 1>,
                          (unsigned)((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0,
                          l.stream, l.p);
