@@ -343,8 +343,10 @@ PKV_API size_t pkv_shared_prefix_workspace_bytes(const pkv_cache_desc* desc, int
  * batches, where the separate passes cost more than they save, take one
  * kernel that reads the prefix for each sequence.  Results are bitwise
  * repeatable.  Values of the prefix behind a sequence's length, but inside
- * another's, meet a weight of zero: they must be finite.  Other arguments and
- * guarantees as for pkv_paged_decode_attention. */
+ * another's, meet a weight of zero: they must be finite.  A prefix block or
+ * table entry outside the pool is a device-detected PKV_ERR_BOUNDS; its
+ * positions are left out, as by pkv_paged_decode_attention.  Other arguments
+ * and guarantees as for that call. */
 PKV_API pkv_status pkv_paged_decode_attention_shared_prefix(
     const pkv_cache_desc* desc, const void* q, const void* k_cache,
     const void* v_cache, const int32_t* prefix_blocks,

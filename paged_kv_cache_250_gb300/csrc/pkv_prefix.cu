@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bb = wk.buf(t, i), u = wk.use(t, i);
             const int npg = min(kPages, p.npb - wk.block(t, i) * kPages);
             int blk = t == 0 ? cur0 : cur1;
-            if (lane < npg && (blk < 0 || blk >= p.NB)) {  // read as zeros, past the pool
+            if (lane < npg && (blk < 0 || blk >= p.NB)) {  // zeros, past the pool
               if (v == 0) report_error(p.err_word, PKV_ERR_BOUNDS);
               blk = p.NB;
             }
@@ -388,20 +388,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int all_vis = __reduce_min_sync(0xffffffffu, vis);
     float m_ref = -INFINITY, l_sum = 0.f;
     for (int i = 0; i < nt; ++i, tok0 += tok_step) {
+      // a block outside the pool (reported by the copy warp, zeros in shared
+      // memory) is left out: bit pg stands for the step's page pg
+      const int pg = tok0 / kPageSize + lane;
+      const int entry = lane < kPages && pg < p.npb ? p.prefix_blocks[pg] : 0;
       ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
       if (!ok) break;
       tc_fence_after();
-      const bool full = tok0 + kTok - 1 <= all_vis;
+      const uint32_t bad = __ballot_sync(0xffffffffu, entry < 0 || entry >= p.NB);
+      const bool full = tok0 + kTok - 1 <= all_vis && bad == 0;
+      // last position the row sees in the quarter's pages
+      auto vis_of = [&](int qq, int half) { return (bad >> (2 * qq + half)) & 1 ? -1 : vis; };
       uint32_t sa[32], sb[32];
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       auto qmax = [&](auto mc, const uint32_t (&sq)[32], int qq) {
         const int t0 = tok0 + 32 * qq;
+        [[maybe_unused]] const int last[2] = {vis_of(qq, 0), vis_of(qq, 1)};
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float a = __uint_as_float(sq[2 * e]), c = __uint_as_float(sq[2 * e + 1]);
           if constexpr (decltype(mc)::value) {
-            if (t0 + 2 * e > vis) a = -INFINITY;
-            if (t0 + 2 * e + 1 > vis) c = -INFINITY;
+            if (t0 + 2 * e > last[e >> 3]) a = -INFINITY;
+            if (t0 + 2 * e + 1 > last[e >> 3]) c = -INFINITY;
           }
           m4[e & 3] = max3(m4[e & 3], a, c);
         }
@@ -450,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       uint32_t hi[16], lo[16];
       auto qp = [&](auto mc, const uint32_t (&sq)[32], int qq) {
+        [[maybe_unused]] const int last[2] = {vis_of(qq, 0), vis_of(qq, 1)};
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 y = f2_split(fma2(f2(__uint_as_float(sq[2 * e]),
@@ -457,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float p0 = ex2(y.x), p1 = ex2(y.y);
           if constexpr (decltype(mc)::value) {
             const int tk = tok0 + 32 * qq + 2 * e;
-            if (tk > vis) p0 = 0.f;
-            if (tk + 1 > vis) p1 = 0.f;
+            if (tk > last[e >> 3]) p0 = 0.f;
+            if (tk + 1 > last[e >> 3]) p1 = 0.f;
           }
           const uint64_t pp = f2(p0, p1);
           acc[e & 3] = add2(acc[e & 3], pp);
