@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int seen = *max_len;
+  const int pages = (seen + kPageSize - 1) / kPageSize;  // those behind are not looked up
   if (blockIdx.x == 0 && tid == 0) *p.seen = seen;  // for the merge
   const PrefixLine line = line_of(p, seen);
   const int64_t lo = blockIdx.x < line.n && seen > 0 ? line.share(blockIdx.x) : 0;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int streams = wk.s.two ? 1 : 2;
       auto entry = [&](int t, int i) -> int {  // lane l < 8: page l's block
         const int pg = wk.block(t, i) * kPages + lane;
-        return lane < kPages && t < streams && i < wk.count(t) && pg < p.npb
+        return lane < kPages && t < streams && i < wk.count(t) && pg < pages
                    ? p.prefix_blocks[pg] : 0;
       };
       int cur0 = entry(0, 0), cur1 = entry(1, 0);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < streams; ++t) {
             if (i >= wk.count(t)) continue;
             const int bb = wk.buf(t, i), u = wk.use(t, i);
-            const int npg = min(kPages, p.npb - wk.block(t, i) * kPages);
+            const int npg = min(kPages, pages - wk.block(t, i) * kPages);
             int blk = t == 0 ? cur0 : cur1;
             if (lane < npg && (blk < 0 || blk >= p.NB)) {  // zeros, past the pool
               if (v == 0) report_error(p.err_word, PKV_ERR_BOUNDS);
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a block outside the pool (reported by the copy warp, zeros in shared
       // memory) is left out: bit pg stands for the step's page pg
       const int pg = tok0 / kPageSize + lane;
-      const int entry = lane < kPages && pg < p.npb ? p.prefix_blocks[pg] : 0;
+      const int entry = lane < kPages && pg < pages ? p.prefix_blocks[pg] : 0;
       ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
       if (!ok) break;
       tc_fence_after();

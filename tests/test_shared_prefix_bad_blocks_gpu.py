@@ -49,3 +49,18 @@ def test_a_bad_block_is_left_out(case, pages):
     check(o[:12], torch.stack([r[0] for r in ref]), torch.stack([r[1] for r in ref]), "f32",
           str(pages[:8]))
     assert torch.equal(o, shared(p, q, ws=ws))
+
+
+@pytest.mark.parametrize("longest", [1, 16, 17, 100, 128, 1030])
+@pytest.mark.parametrize("prefix,Hq,Hkv,d,B,passes", [(1040, 8, 8, 128, 12, True),
+                                                      (1040, 32, 4, 128, 40, True),
+                                                      (1040, 8, 1, 64, 3, False)])
+def test_blocks_behind_every_length_are_not_looked_up(longest, prefix, Hq, Hkv, d, B, passes):
+    p = Paged([longest - i % 2 for i in range(B)], Hq, Hkv, d, "bf16", 113, prefix=prefix)
+    assert own_pass(p) == passes
+    p.prefix_blocks[-(-longest // PAGE):] = -1
+    q = p.queries(B, 114, 2.0)
+    o = shared(p, q)
+    assert p.err.item() == 0
+    ref = [without(p, q, b, []) for b in range(3)]
+    check(o[:3], torch.stack([r[0] for r in ref]), torch.stack([r[1] for r in ref]), "f32")
