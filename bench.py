@@ -490,9 +490,9 @@ def committed_traffic(workload):
 
 # the sources the decode and append kernels are built from (the prefill and
 # block-copy kernels do not change them)
-DECODE_SOURCES = ("pkv_decode_impl.cuh", "pkv_device.cuh", "pkv_internal.h", "pkv_api.cu",
-                  "pkv_append.cu", "pkv_decode_bf16.cu", "pkv_decode_f16.cu", "pkv_decode_e4m3.cu",
-                  "pkv_decode_e4m3_tok.cu")
+DECODE_SOURCES = ("pkv_decode_impl.cuh", "pkv_device.cuh", "pkv_hd.h", "pkv_internal.h",
+                  "pkv_api.cu", "pkv_append.cu", "pkv_decode_bf16.cu", "pkv_decode_f16.cu",
+                  "pkv_decode_e4m3.cu", "pkv_decode_e4m3_tok.cu")
 
 
 def kernel_source_hash():

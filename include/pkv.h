@@ -297,8 +297,8 @@ PKV_API pkv_status pkv_paged_decode_attention_window(
  *   s = scale q.k;  s = softcap tanh(s / softcap) if softcap > 0;
  *   s = s + alibi_slopes[hq] (u - t) if alibi_slopes is given.
  *   window, sinks as for pkv_paged_decode_attention_window (0: no window).
- *   softcap       0 (no cap), or between 2^-10 and 2^10.  The tanh is off by
- *                 2^-22 of the cap at most.
+ *   softcap       0 (no cap), or between 2^-10 and 2^10.  The capped score is
+ *                 off by less than 2^-21 of the cap, so 2^-11 under the widest.
  *   alibi_slopes  device fp32 [num_q_heads], or NULL.
  * With neither, the call is pkv_paged_decode_attention (or _window) itself.
  * Other arguments, workspace and guarantees as for
@@ -325,9 +325,10 @@ PKV_API size_t pkv_shared_prefix_workspace_bytes(const pkv_cache_desc* desc, int
  * same blocks (a system prompt, a document, samples of one prompt; [KVFA]
  * PagedAttention section, [AP] "Paged attention: stop reserving empty
  * tables": sequences point at the same physical blocks for a shared
- * beginning).  The prefix is read once for the whole batch: a dense product
- * of all query rows of a KV head with its blocks on the tensor cores
- * (tcgen05), merged with each sequence's attention over its own blocks.
+ * beginning).  The prefix is read once for every 256 query rows of a KV head
+ * (256 / group sequences; larger batches find it in L2 again) instead of once
+ * per sequence: a dense product of the rows with its blocks on the tensor
+ * cores (tcgen05), merged with each sequence's attention over its own blocks.
  *   prefix_blocks      device int32 [num_prefix_blocks]: the blocks of
  *                      positions 0 .. 16 num_prefix_blocks - 1 of every
  *                      sequence.

@@ -18,7 +18,7 @@ memory and streams.  The functions carry the C names:
                                   distance bias, or both
     pkv_paged_decode_attention_shared_prefix  decode for a batch whose
                                   sequences begin with the same blocks, read
-                                  once for all of them
+                                  once for every 256 query rows of a KV head
     pkv_shared_prefix_workspace_bytes  workspace size for that call
     pkv_paged_prefill_attention   a chunk of new tokens per sequence, causal,
                                   on the tensor cores (tcgen05)
@@ -499,8 +499,9 @@ def pkv_paged_decode_attention_shared_prefix(desc: CacheDesc, q: torch.Tensor,
                                              stream=None) -> None:
     """As pkv_paged_decode_attention for sequences that all begin with the
     blocks prefix_blocks (int32 [num_prefix_blocks]), which are read once for
-    the batch; block_tables holds whole tables, whose entries for the prefix
-    are not read, and context_lens whole lengths."""
+    every 256 query rows of a KV head (short prefixes and small batches: once per
+    sequence); block_tables holds whole tables, whose entries for the prefix are
+    not read, and context_lens whole lengths."""
     lib = _lib or load_library()
     dev = q.get_device()
     if not _is_current(dev):

@@ -197,8 +197,8 @@ pkv_status encode_q_map(CUtensorMap* map, const void* q, const pkv_cache_desc* d
              : PKV_ERR_CUDA;
 }
 
-// A cap is 0 (none) or between 2^-10 and 2^10: the tanh's error is 2^-22 of the
-// cap, and a wider cap bends no score that fp32 tells apart anyway.
+// A cap is 0 (none) or between 2^-10 and 2^10: the tanh's error is up to 2^-21 of
+// the cap, so under a wider one a score could be more than 2^-11 off.
 pkv_status bias_checks(float softcap, const float* slopes) {
   if (softcap != 0.f && !(softcap >= 0x1p-10f && softcap <= 0x1p10f)) return PKV_ERR_INVALID_ARG;
   if (!aligned(slopes, 4)) return PKV_ERR_INVALID_ARG;

@@ -163,10 +163,13 @@ __device__ __forceinline__ float rcp(float x) {  // 1 / x (PTX rcp.approx; inf g
 // A score x capped by a tanh, both in log2 units: with y = s / cap and
 // z = 2 y log2e = x z_of_x (z_of_x = 2 / cap),  tanh(y) = 1 - 2 / (1 + 2^z):
 // two special-function instructions, and the ends come out as +-1 by themselves
-// (2^z = inf or 0).  The error is about 2^-22 of the cap, whatever y is: 2^-16
-// of a score's unit under a cap of 64, as much as a weight's own rounding to its
-// 16-bit pair.  (The series for small y would keep every bit under wide caps too;
-// it cost the E4M3 decode 9 % and the prefill kernel registers.)
+// (2^z = inf or 0).  The error stays below 2^-21 of the cap, whatever y is (in
+// 2^-24 of it, at the worst y: ex2's 2^-22 and z's two roundings 2, the sum 1.7,
+// rcp's last place 2, the last step 1.4): 2^-15 of a score's unit under a cap of
+// 64, about a weight's own rounding to its 16-bit pair, and 2^-11 under the widest
+// cap, 2^10, where it is what limits a 32-bit output.  (The series for small y
+// would keep every bit under wide caps too; it cost the E4M3 decode 9 % and the
+// prefill kernel registers.)
 __device__ __forceinline__ float cap_score(float x, float z_of_x, float cap_log2) {
   return fmaf(rcp(1.f + ex2(x * z_of_x)), -2.f * cap_log2, cap_log2);
 }

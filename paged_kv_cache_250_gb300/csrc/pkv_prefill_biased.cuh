@@ -20,11 +20,11 @@
 // 1399 us, against 1488 with the prefill kernel's steps of 128 tokens and one
 // buffer, where a tile's softmax and its products take turns; 1370 with the MMAs
 // issued behind elect.sync.  12 sequences of up to 700 rows with cap and slopes:
-// 189, before 208.  A step takes about 3500 cycles, of which its 32 MMAs are 1790
-// (N 64: 48 each, N 128: 64) and the special-function unit's work for the two
-// softmax warps of a scheduler about 2050; the latency of those two warps (issue
-// 43 %) is what is left.  Twice the warps, two groups per tile that take the steps
-// in turn and hand the reference maximum over, took 1482 us (96 registers).
+// 189, before 208.  A step takes about 3500 cycles.  No pipe is full in the long
+// case (tensor 45 %, special functions 46 %, issue 45 %): what is left is the
+// latency of the two softmax warps of a scheduler.  Twice the warps, two groups per
+// tile that take the steps in turn and hand the reference maximum over, took
+// 1482 us (96 registers).
 #pragma once
 
 #include <atomic>
@@ -295,7 +295,9 @@ __device__ __forceinline__ bool softmax_steps(const Cta& c, int N, int t, int tt
 #pragma unroll
       for (int qq = 0; qq < 2; ++qq) {
         const int t0 = tok0 + 32 * qq;
-        // the distance bias of two tokens, and the cap
+        // the distance bias of two tokens, and the cap; stepped on by adding, so the
+        // last of 32 tokens carries 16 roundings of its bias where a product for each
+        // would carry one
         [[maybe_unused]] uint64_t add = f2(w.slope2 * (float)(t0 - w.vis),
                                            w.slope2 * (float)(t0 + 1 - w.vis));
         if constexpr (kCap) add = add2(cap2, add);

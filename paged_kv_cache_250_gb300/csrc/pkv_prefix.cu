@@ -12,8 +12,8 @@
 //
 // prefix_kernel.  The (pair of 128-row tiles, KV head, block) units lie on one
 // line, cut into equal shares, one per CTA of at most one CTA per SM; a share
-// crosses a few segments (pair, KV head) and leaves one partial in each.  Roles
-// hand over through mbarriers, as in the prefill kernel:
+// crosses a few segments (pair, KV head) and leaves one partial in each (see
+// pkv_prefix_line.h).  Roles hand over through mbarriers, as in the prefill kernel:
 //   warps 0-3, 4-7  softmax of stream 0, 1: one row per thread, TMEM lane t;
 //   warp 8          issues the MMAs; warp 9 the tensor copies.
 // A stream is a row tile with its accumulator.  Two tiles of rows share every
@@ -30,7 +30,7 @@
 // PFLOP/s (1.38 with the second product of P); 167 us before the MMAs were issued
 // behind elect.sync.  Equal shares replaced a grid of (pair, head, split) with
 // the splits picked by a search, which took 299 us for the whole call (227 at
-// that step, now 194).  Measured and not kept: steps of 64 tokens with two score
+// that step, now 193).  Measured and not kept: steps of 64 tokens with two score
 // buffers, as in the biased prefill kernel (193 us for the call against 195: the
 // softmax warps' latency bounds both), more registers for the softmax warps by
 // setmaxnreg (180, 176 at the time).
@@ -38,17 +38,16 @@
 // own_kernel.  One warp per CTA and per chunk of one sequence's own pages of
 // one KV head: the page ring, MMAs and softmax of the single-token decode
 // kernel's warp, with nothing to hand over at a segment's end; bound by HBM
-// (269 MB of own pages, 256 sequences of up to 512 tokens: 49 us alone and cold,
-// 5.5 TB/s; the decode kernel's form, which leaves a partial per share, took
-// 127).  It depends on
-// nothing the prefix kernel writes and needs little of an SM (a 24 KB ring), so
-// its first CTAs start beside the prefix kernel's and the rest as SMs come
-// free.  All of it beside the prefix kernel, from a queue, was slower: the
-// prefix then took 270 us and the call 301 (227 at the time).
+// (269 MB of own pages, 256 sequences of up to 512 tokens: 51 us alone and cold,
+// 5.5 TB/s of DRAM traffic; the decode kernel's form, which leaves a partial per
+// share, took 127).  It depends on nothing the prefix kernel writes and needs little
+// of an SM (a 24 KB ring), so its first CTAs start beside the prefix kernel's and
+// the rest as SMs come free.  All of it beside the prefix kernel, from a queue, was
+// slower: the prefix then took 270 us and the call 301 (227 at the time).
 //
 // prefix_merge_kernel.  A warp per row adds the parts in a fixed order, four
 // warps where rows are few and their parts many; bound by the latency of the
-// parts, which are in L2 (16 us alone and cold, about 5 in the same call).
+// parts, which are in L2 (17 us alone and cold, about 5 in the same call).
 #include <atomic>
 
 #include "pkv_device.cuh"

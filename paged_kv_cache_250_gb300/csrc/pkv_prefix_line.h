@@ -28,11 +28,18 @@ PKV_HD int64_t prefix_cost(int32_t Hkv, int64_t blocks, int32_t pairs, int last_
 }
 
 // CTAs to launch for a prefix of the given whole cost on `sms` SMs.  In units of
-// cost 2 the longest share is m = ceil(units / sms); while m is small, as many CTAs
-// as shares of m take, no more: fewer partials in the same time (64 sequences
-// behind 8192 tokens, m = 4: 128 CTAs 41.1 us, 152 43.2).  The count falls where m
-// steps up, so it belongs to the launch alone: a cut of less than the whole prefix
-// (see PrefixLine) goes by the CTAs that were launched.
+// cost 2 the longest share is m = ceil(units / sms); up to m = 4, as many CTAs as
+// shares of m take, no more: fewer partials in the same time.  64 sequences with own
+// parts of up to 512 tokens, 32/8 heads of 128, 152 SMs, a call with that many CTAs
+// and with one per SM, in us:
+//   m  prefix  CTAs                 m  prefix  CTAs
+//   2    2560    80  31.0 / 37.1    4    7424   116  38.9 / 41.7
+//   2    3584   112  34.8 / 37.8    4    8192   128  40.2 / 42.3
+//   3    4992   104  35.9 / 39.6    5    9856   124  41.7 / 43.9
+//   3    6144   128  38.3 / 40.5    8   16384   128  49.5 / 49.7
+// (m = 5 to 7 would gain 2.2, 1.8 and 1.4 us too; the limit has not followed.)  The
+// count falls where m steps up, so it belongs to the launch alone: a cut of less than
+// the whole prefix (see PrefixLine) goes by the CTAs that were launched.
 PKV_HD int64_t prefix_ctas(int64_t cost, int32_t sms) {
   const int64_t units = cost >> 1 > 0 ? cost >> 1 : 1;
   for (int m = 1; m <= 4; ++m)
