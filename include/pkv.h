@@ -312,6 +312,152 @@ PKV_API pkv_status pkv_paged_decode_attention_biased(
     pkv_dtype out_dtype, void* workspace, size_t workspace_bytes,
     pkv_stream_t stream);
 
+/* Bytes of device workspace pkv_paged_decode_attention_scored needs on the
+ * current device: that of the plain call, and room for one fp32 score per
+ * (sequence, query head, table position).  Zero-filled once before its first
+ * use; serves every call with the same descriptor, a batch of at most B and a
+ * max_blocks_per_seq of at most this one (pass its full size); other rules as
+ * for pkv_decode_workspace_bytes.  Returns 0 on invalid arguments or without a
+ * device. */
+PKV_API size_t pkv_scored_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                  int32_t max_blocks_per_seq,
+                                  int32_t max_context_len_hint);
+
+/* pkv_paged_decode_attention that also adds up the attention weight each cached
+ * row receives, for pkv_kv_evict ([KVFA] eviction paragraph: rows that receive
+ * little attention can go).  With p_hq[u] the softmax weight of query head hq
+ * on position u, the weight of u under KV head h becomes
+ *   w[u] = decay w[u] + sum of p_hq[u] over the query heads hq of h
+ * (fp32).  The newest position's weight (context_lens[b] - 1) is set to its
+ * sum, so a row need not be cleared when it is appended; with decay 0 every
+ * position's is, whatever was there (the first call after a prompt).
+ *   weights       device fp32 [num_blocks][num_kv_heads][page_size], beside the
+ *                 caches: the weight of the row in the same block and slot.
+ *                 Entries of positions the call does not see stay as they are.
+ *   decay         0 .. 1: 1 sums over all steps, less forgets older ones.
+ *   workspace     of at least pkv_scored_workspace_bytes() bytes.
+ * A block that two sequences of the call share gets the sum of one of them, or
+ * a mixture (their updates race); `out` is right all the same.  pkv_copy_blocks
+ * does not copy weights.  Other arguments and guarantees as for
+ * pkv_paged_decode_attention; the weights are bitwise repeatable too. */
+PKV_API pkv_status pkv_paged_decode_attention_scored(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, float* weights, float decay, int32_t batch,
+    int32_t max_blocks_per_seq, int32_t max_context_len_hint, float scale,
+    void* out, pkv_dtype q_dtype, pkv_dtype out_dtype, void* workspace,
+    size_t workspace_bytes, pkv_stream_t stream);
+
+/* Most nodes of a tree, and most steps of a path. */
+#define PKV_MAX_TREE 64
+
+/* Bytes of device workspace pkv_paged_tree_attention needs on the current
+ * device.  It need not be cleared, and serves every call with the same
+ * descriptor.  Returns 0 on invalid arguments or without a device. */
+PKV_API size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                int32_t max_q_len, int32_t max_blocks_per_seq);
+
+/* Decode attention for a tree of drafted tokens per sequence ([KVFA]
+ * speculative-decoding section: the target model scores the prefix and the
+ * drafted tokens in one forward pass; here the drafts branch, so several
+ * continuations are verified at once).  Sequence b's tree has n_b nodes (0 ..
+ * PKV_MAX_TREE), whose K and V already lie in the cache at its last n_b
+ * positions: node i at position context_lens[b] - n_b + i.  Node j attends to
+ * every position before the tree and to the nodes its mask names.
+ *   q             [total_q][num_q_heads][head_dim] of q_dtype (= cache_dtype);
+ *                 sequence b's nodes are rows q_start[b] .. q_start[b + 1] - 1.
+ *   q_start       int32 [batch + 1], device, as for pkv_paged_prefill_attention.
+ *   max_q_len     host: an upper bound on n_b, 0 .. PKV_MAX_TREE.
+ *   tree_mask     device int64 [total_q]: bit i of a row's word is set where
+ *                 the row sees node i of its sequence's tree (its ancestors'
+ *                 bits and its own); bits from n_b on are ignored.  A row that
+ *                 sees no position at all gets a zero output row.
+ *   scale         > 0 (the softmax scale).
+ *   out           [total_q][num_q_heads][head_dim] of out_dtype (F16 | BF16 |
+ *                 F32).
+ *   workspace     at least pkv_tree_workspace_bytes() bytes, 256-byte aligned,
+ *                 not shared with calls that overlap.
+ * 16-bit caches (E4M3 returns PKV_ERR_UNSUPPORTED, and so does a max_q_len above
+ * PKV_MAX_TREE or a batch above 4096).  A sequence whose node count or length breaks the rules
+ * is a device-detected PKV_ERR_BOUNDS and its rows are not written.  A table
+ * entry outside the pool is PKV_ERR_BOUNDS; its positions are left out, as by
+ * pkv_paged_decode_attention.  Values (V) of nodes that some row of the tree
+ * sees meet a weight of zero in the others: they must be finite.  Keys behind
+ * a mask, and values that no row sees, may be anything.  Results are bitwise
+ * repeatable. */
+PKV_API pkv_status pkv_paged_tree_attention(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* q_start, int32_t batch,
+    int32_t total_q, int32_t max_q_len, const int64_t* tree_mask,
+    int32_t max_blocks_per_seq, float scale, void* out, pkv_dtype q_dtype,
+    pkv_dtype out_dtype, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream);
+
+/* Keep the accepted path of each tree: the K and V rows (and per-token scales)
+ * of its nodes move up behind the sequence's past, in the path's order.
+ *   q_start       as for pkv_paged_tree_attention: n_b nodes in the last n_b of
+ *                 context_lens[b] positions; P_b = context_lens[b] - n_b.
+ *   path          device int32 [batch][max_path]: entry i of sequence b, i <
+ *                 path_lens[b], is the node whose row goes to position P_b + i
+ *                 (0 .. n_b - 1, in any order).  Every row is read before any
+ *                 is written.
+ *   max_path      0 .. PKV_MAX_TREE (more returns PKV_ERR_UNSUPPORTED).
+ *   path_lens     device int32 [batch], 0 .. min(n_b, max_path).
+ *   new_context_lens  device int32 [batch] or NULL: P_b + path_lens[b].  Must
+ *                 not overlap the other arrays of the call.
+ * Rows behind the new length keep what they held.  A sequence whose lengths
+ * break the rules is a device-detected PKV_ERR_BOUNDS and stays as it is, its
+ * entry of new_context_lens too; a node or block out of range is PKV_ERR_BOUNDS
+ * and that step's row is not moved.  Blocks that receive a row must belong to
+ * one sequence of the call (copy shared ones first: pkv_copy_blocks).  All cache
+ * types. */
+PKV_API pkv_status pkv_kv_accept_path(
+    const pkv_cache_desc* desc, void* k_cache, void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens,
+    const int32_t* q_start, const int32_t* path, const int32_t* path_lens,
+    int32_t max_path, int32_t batch, int32_t max_blocks_per_seq,
+    int32_t* new_context_lens, pkv_stream_t stream);
+
+/* Evict cached rows by their accumulated attention weight ([KVFA] eviction
+ * paragraph): of the context_lens[b] = n rows of a sequence, `budget` stay under
+ * each KV head, which chooses its own.  Kept first are the rows whose token is
+ * one of the sequence's first `sinks` or its last `recent`; then those with the
+ * largest weight (NaN above infinity; of equal ones the row at the lower index).
+ * Kept rows at indices below `budget` stay in place; those behind move, in
+ * order, into the places of the evicted ones (K, V, per-token scales, weight and
+ * position).  So a cache's rows lose their order (attention does not see it:
+ * keys are rotated when they are appended), and `positions` says which token a
+ * row belongs to.  A sequence of at most `budget` rows keeps them all.
+ *   weights       as for pkv_paged_decode_attention_scored.
+ *   positions     device int32 [num_blocks][num_kv_heads][page_size]: the token
+ *                 (0, 1, ...) of the row in the same block and slot.
+ *   context_lens  device int32 [batch], rows cached now.
+ *   old_lens      device int32 [batch], the rows whose positions are known: the
+ *                 new_context_lens of the sequence's last call, or 0 before the
+ *                 first.  Rows at or past it hold the sequence's last tokens in
+ *                 order, up to num_tokens[b] - 1, and their positions are
+ *                 written by this call.
+ *   num_tokens    device int32 [batch], tokens the sequence has had in all (at
+ *                 least context_lens[b]).
+ *   budget        >= 1; sinks, recent >= 0 and sinks + recent <= budget.
+ *   new_context_lens  device int32 [batch]: min(n, budget).  Must not overlap
+ *                 the other arrays of the call.
+ * Rows at or behind the new length keep what they held.  A sequence whose
+ * lengths break the rules is a device-detected PKV_ERR_BOUNDS and stays as it
+ * is, its entry of new_context_lens too.  A table entry outside the pool is
+ * PKV_ERR_BOUNDS: its rows are the first to go and are never read or written.
+ * Blocks must belong to one sequence of the call (copy shared ones first:
+ * pkv_copy_blocks).  Tables of up to 24576 blocks per sequence (more returns
+ * PKV_ERR_UNSUPPORTED).  All cache types; no workspace. */
+PKV_API pkv_status pkv_kv_evict(
+    const pkv_cache_desc* desc, void* k_cache, void* v_cache, float* weights,
+    int32_t* positions, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* old_lens,
+    const int32_t* num_tokens, int32_t batch, int32_t max_blocks_per_seq,
+    int32_t budget, int32_t sinks, int32_t recent, int32_t* new_context_lens,
+    pkv_stream_t stream);
+
 /* Bytes of device workspace pkv_paged_decode_attention_shared_prefix needs on
  * the current device; rules as for pkv_decode_workspace_bytes (zero-filled
  * once, serves every batch of at most B and any number of prefix blocks).

@@ -16,6 +16,14 @@ memory and streams.  The functions carry the C names:
                                   attention sinks
     pkv_paged_decode_attention_biased  decode with scores capped by a tanh, a
                                   distance bias, or both
+    pkv_paged_decode_attention_scored  decode that adds up the attention weight
+                                  each cached row receives
+    pkv_scored_workspace_bytes    workspace size for that call
+    pkv_kv_evict                  keep the rows with the largest weights, the
+                                  first and the most recent ones
+    pkv_paged_tree_attention      a tree of drafted tokens per sequence (tcgen05)
+    pkv_tree_workspace_bytes      workspace size for that call
+    pkv_kv_accept_path            keep the rows of a path through the tree
     pkv_paged_decode_attention_shared_prefix  decode for a batch whose
                                   sequences begin with the same blocks, read
                                   once for every 256 query rows of a KV head
@@ -58,6 +66,9 @@ __all__ = [
     "pkv_decode_step_fused", "pkv_paged_prefill_attention", "pkv_kv_append_rope",
     "pkv_paged_decode_attention_biased", "pkv_paged_prefill_attention_biased",
     "pkv_paged_decode_attention_shared_prefix", "pkv_shared_prefix_workspace_bytes",
+    "pkv_paged_decode_attention_scored", "pkv_scored_workspace_bytes", "pkv_kv_evict",
+    "pkv_paged_tree_attention", "pkv_tree_workspace_bytes", "pkv_kv_accept_path",
+    "PKV_MAX_TREE",
     "PKV_ROPE_INTERLEAVED",
     "PKV_OK", "PKV_ERR_INVALID_ARG", "PKV_ERR_UNSUPPORTED", "PKV_ERR_WORKSPACE",
     "PKV_ERR_CUDA", "PKV_ERR_BOUNDS", "PKV_ERR_TIMEOUT",
@@ -70,6 +81,7 @@ PKV_ERR_CUDA, PKV_ERR_BOUNDS, PKV_ERR_TIMEOUT = 4, 5, 6
 PKV_F16, PKV_BF16, PKV_FP8_E4M3, PKV_F32, PKV_FP8_E4M3_TOKEN = 0, 1, 2, 3, 4
 PKV_STEP_OVERLAP = 1
 PKV_ROPE_INTERLEAVED = 1
+PKV_MAX_TREE = 64
 
 EXPORTED_SYMBOLS = (
     "pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_attention",
@@ -79,6 +91,8 @@ EXPORTED_SYMBOLS = (
     "pkv_decode_workspace_bytes_multi", "pkv_kv_append_rope",
     "pkv_paged_decode_attention_biased", "pkv_paged_prefill_attention_biased",
     "pkv_paged_decode_attention_shared_prefix", "pkv_shared_prefix_workspace_bytes",
+    "pkv_paged_decode_attention_scored", "pkv_scored_workspace_bytes", "pkv_kv_evict",
+    "pkv_paged_tree_attention", "pkv_tree_workspace_bytes", "pkv_kv_accept_path",
 )
 PKV_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -173,6 +187,20 @@ def load_library():
         lib.pkv_paged_decode_attention_shared_prefix.argtypes = [D, P, P, P, P, I32, P, P, I32,
                                                                  I32, I32, F, P, I32, I32, P, SZ,
                                                                  P]
+        lib.pkv_scored_workspace_bytes.restype = SZ
+        lib.pkv_scored_workspace_bytes.argtypes = [D, I32, I32, I32]
+        lib.pkv_paged_decode_attention_scored.restype = I32
+        lib.pkv_paged_decode_attention_scored.argtypes = [D, P, P, P, P, P, P, F, I32, I32, I32,
+                                                          F, P, I32, I32, P, SZ, P]
+        lib.pkv_tree_workspace_bytes.restype = SZ
+        lib.pkv_tree_workspace_bytes.argtypes = [D, I32, I32, I32]
+        lib.pkv_paged_tree_attention.restype = I32
+        lib.pkv_paged_tree_attention.argtypes = [D, P, P, P, P, P, P, I32, I32, I32, P, I32, F, P,
+                                                 I32, I32, P, SZ, P]
+        lib.pkv_kv_accept_path.restype = I32
+        lib.pkv_kv_accept_path.argtypes = [D, P, P, P, P, P, P, P, I32, I32, I32, P, P]
+        lib.pkv_kv_evict.restype = I32
+        lib.pkv_kv_evict.argtypes = [D, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, P, P]
         lib.pkv_copy_blocks.restype = I32
         lib.pkv_copy_blocks.argtypes = [D, P, P, P, P, I32, P]
         lib.pkv_kv_bytes_per_token.restype = U64
@@ -477,6 +505,168 @@ def pkv_paged_decode_attention_biased(desc: CacheDesc, q: torch.Tensor, k_cache:
         _on(workspace, dev, "workspace"), workspace.nbytes, _stream_on(stream, dev))
     if st:
         raise PkvError(st, "pkv_paged_decode_attention_biased")
+
+
+def pkv_scored_workspace_bytes(desc: CacheDesc, batch: int, max_blocks_per_seq: int,
+                               max_context_len_hint: int = 0) -> int:
+    lib = load_library()
+    return int(lib.pkv_scored_workspace_bytes(ctypes.byref(desc), int(batch),
+                                              int(max_blocks_per_seq),
+                                              int(max_context_len_hint)))
+
+
+def _row_pool(t: torch.Tensor, dtype, desc: CacheDesc, dev: int, name: str) -> int:
+    """Device address of a pool with one entry per cached row."""
+    if t.dtype is not dtype or t.numel() != desc.num_blocks * desc.num_kv_heads * desc.page_size:
+        raise ValueError(f"{name} must be {dtype} [num_blocks][Hkv][page_size]")
+    return _on(t, dev, name)
+
+
+def pkv_paged_decode_attention_scored(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,
+                                      v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                      context_lens: torch.Tensor, weights: torch.Tensor,
+                                      scale: float, out: torch.Tensor, workspace: torch.Tensor,
+                                      decay: float = 1.0, max_context_len_hint: int = 0,
+                                      stream=None) -> None:
+    """As pkv_paged_decode_attention; weights (fp32 [num_blocks][Hkv][16]) of the
+    rows seen become decay * weights + the attention weight of the KV head's query
+    heads, the newest row's (and with decay 0 all of them) the latter alone."""
+    lib = _lib or load_library()
+    dev = q.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_paged_decode_attention_scored(
+                desc, q, k_cache, v_cache, block_tables, context_lens, weights, scale, out,
+                workspace, decay, max_context_len_hint, stream)
+    B, mbs = _batch_of(desc, q, out, block_tables, context_lens)
+    st = lib.pkv_paged_decode_attention_scored(
+        ctypes.byref(desc), _on(q, dev, "q"), _on(k_cache, dev, "k_cache"),
+        _on(v_cache, dev, "v_cache"), _on(block_tables, dev, "block_tables"),
+        _on(context_lens, dev, "context_lens"),
+        _row_pool(weights, torch.float32, desc, dev, "weights"), float(decay), B, mbs,
+        int(max_context_len_hint), float(scale), _on(out, dev, "out"),
+        _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
+        _on(workspace, dev, "workspace"), workspace.nbytes, _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_paged_decode_attention_scored")
+
+
+def pkv_kv_evict(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 weights: torch.Tensor, positions: torch.Tensor, block_tables: torch.Tensor,
+                 context_lens: torch.Tensor, old_lens: torch.Tensor, num_tokens: torch.Tensor,
+                 budget: int, sinks: int, recent: int, new_context_lens: torch.Tensor,
+                 stream=None) -> None:
+    """Keep `budget` rows of each sequence under each KV head: those of its first
+    `sinks` and last `recent` tokens, then those with the largest weights.  weights
+    (fp32) and positions (int32: the token of a row) are [num_blocks][Hkv][16];
+    context_lens, old_lens (rows whose positions are known), num_tokens (tokens in
+    all) and new_context_lens (written) int32 [B]."""
+    lib = _lib or load_library()
+    dev = k_cache.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_kv_evict(desc, k_cache, v_cache, weights, positions, block_tables,
+                                context_lens, old_lens, num_tokens, budget, sinks, recent,
+                                new_context_lens, stream)
+    i32 = torch.int32
+    if (block_tables.dtype is not i32 or context_lens.dtype is not i32
+            or old_lens.dtype is not i32 or num_tokens.dtype is not i32
+            or new_context_lens.dtype is not i32):
+        raise ValueError("block_tables, context_lens, old_lens, num_tokens and "
+                         "new_context_lens must be int32")
+    B, mbs = block_tables.shape
+    if not (context_lens.numel() == old_lens.numel() == num_tokens.numel()
+            == new_context_lens.numel() == B):
+        raise ValueError("the lengths need one entry per sequence")
+    st = lib.pkv_kv_evict(
+        ctypes.byref(desc), _on(k_cache, dev, "k_cache"), _on(v_cache, dev, "v_cache"),
+        _row_pool(weights, torch.float32, desc, dev, "weights"),
+        _row_pool(positions, i32, desc, dev, "positions"), _on(block_tables, dev, "block_tables"),
+        _on(context_lens, dev, "context_lens"), _on(old_lens, dev, "old_lens"),
+        _on(num_tokens, dev, "num_tokens"), B, mbs, int(budget), int(sinks), int(recent),
+        _on(new_context_lens, dev, "new_context_lens"), _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_kv_evict")
+
+
+def pkv_tree_workspace_bytes(desc: CacheDesc, batch: int, max_q_len: int,
+                             max_blocks_per_seq: int) -> int:
+    lib = load_library()
+    return int(lib.pkv_tree_workspace_bytes(ctypes.byref(desc), int(batch), int(max_q_len),
+                                            int(max_blocks_per_seq)))
+
+
+def pkv_paged_tree_attention(desc: CacheDesc, q: torch.Tensor, k_cache: torch.Tensor,
+                             v_cache: torch.Tensor, block_tables: torch.Tensor,
+                             context_lens: torch.Tensor, q_start: torch.Tensor, max_q_len: int,
+                             tree_mask: torch.Tensor, scale: float, out: torch.Tensor,
+                             workspace: torch.Tensor, stream=None) -> None:
+    """q/out: [total_q][Hq][d]; sequence b's nodes are rows q_start[b] ..
+    q_start[b+1]-1 (at most 64), cached at its last positions.  A node sees every
+    position before the tree and node i where bit i of its word in tree_mask (int64
+    [total_q]) is set."""
+    lib = _lib or load_library()
+    dev = q.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_paged_tree_attention(desc, q, k_cache, v_cache, block_tables, context_lens,
+                                            q_start, max_q_len, tree_mask, scale, out, workspace,
+                                            stream)
+    i32 = torch.int32
+    if block_tables.dtype is not i32 or context_lens.dtype is not i32 or q_start.dtype is not i32:
+        raise ValueError("block_tables, context_lens and q_start must be int32")
+    total = q.shape[0]
+    want = (total, desc.num_q_heads, desc.head_dim)
+    if q.shape != want or out.shape != want:
+        raise ValueError("q and out must be [total_q][Hq][d]")
+    if tree_mask.dtype is not torch.int64 or tree_mask.numel() != total:
+        raise ValueError("tree_mask must be int64 with one word per row of q")
+    B, mbs = block_tables.shape
+    if q_start.numel() != B + 1 or context_lens.numel() != B:
+        raise ValueError("q_start needs batch + 1 entries and context_lens batch")
+    st = lib.pkv_paged_tree_attention(
+        ctypes.byref(desc), _on(q, dev, "q"), _on(k_cache, dev, "k_cache"),
+        _on(v_cache, dev, "v_cache"), _on(block_tables, dev, "block_tables"),
+        _on(context_lens, dev, "context_lens"), _on(q_start, dev, "q_start"), B, total,
+        int(max_q_len), _on(tree_mask, dev, "tree_mask"), mbs, float(scale),
+        _on(out, dev, "out"), _DTYPE_CODE.get(q.dtype, -1), _DTYPE_CODE.get(out.dtype, -1),
+        _on(workspace, dev, "workspace"), workspace.nbytes, _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_paged_tree_attention")
+
+
+def pkv_kv_accept_path(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       block_tables: torch.Tensor, context_lens: torch.Tensor,
+                       q_start: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
+                       new_context_lens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The rows of nodes path[b][:path_lens[b]] (int32 [B][max_path]) of each
+    sequence's tree move up behind its past, in that order; new_context_lens (int32
+    [B], written) counts the past and the path."""
+    lib = _lib or load_library()
+    dev = k_cache.get_device()
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return pkv_kv_accept_path(desc, k_cache, v_cache, block_tables, context_lens, q_start,
+                                      path, path_lens, new_context_lens, stream)
+    i32 = torch.int32
+    if (block_tables.dtype is not i32 or context_lens.dtype is not i32
+            or q_start.dtype is not i32 or path.dtype is not i32 or path_lens.dtype is not i32):
+        raise ValueError("block_tables, context_lens, q_start, path and path_lens must be int32")
+    B, mbs = block_tables.shape
+    if (q_start.numel() != B + 1 or context_lens.numel() != B or path_lens.numel() != B
+            or path.dim() != 2 or path.shape[0] != B):
+        raise ValueError("q_start needs batch + 1 entries, context_lens, path and path_lens batch")
+    if new_context_lens is not None and (new_context_lens.dtype is not i32
+                                         or new_context_lens.numel() != B):
+        raise ValueError("new_context_lens must be int32 with one entry per sequence")
+    st = lib.pkv_kv_accept_path(
+        ctypes.byref(desc), _on(k_cache, dev, "k_cache"), _on(v_cache, dev, "v_cache"),
+        _on(block_tables, dev, "block_tables"), _on(context_lens, dev, "context_lens"),
+        _on(q_start, dev, "q_start"), _on(path, dev, "path"), _on(path_lens, dev, "path_lens"),
+        path.shape[1], B, mbs, _on(new_context_lens, dev, "new_context_lens"),
+        _stream_on(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_kv_accept_path")
 
 
 def pkv_shared_prefix_workspace_bytes(desc: CacheDesc, batch: int, num_prefix_blocks: int,

@@ -13,6 +13,8 @@
 #include "pkv_internal.h"
 #include "pkv_prefix_line.h"
 
+static_assert(PKV_MAX_TREE == pkv::kMaxTree && PKV_MAX_TREE == pkv::kMaxPath, "one limit");
+
 namespace {
 
 using pkv::kPageSize;
@@ -242,6 +244,43 @@ bool shared_pays(const pkv_cache_desc* d, int32_t batch, int32_t npb) {
   return batch >= 4 && again >= (int64_t)32 << 20;
 }
 
+// Scored decode: the front of the workspace, one log-sum per (sequence, query
+// head) and one score per (sequence, query head, table position); the plain
+// call's workspace behind it.
+struct ScoredLayout {
+  size_t scores, total;
+};
+ScoredLayout scored_layout(const pkv_cache_desc* d, int32_t batch, int32_t mbs) {
+  const size_t rows = (size_t)batch * d->num_q_heads;
+  ScoredLayout s;
+  s.scores = align256(rows * sizeof(float));
+  s.total = align256(s.scores + rows * mbs * kPageSize * sizeof(float));
+  return s;
+}
+
+// Whether [a, a + n) and [b, b + m) share a byte (null: no).
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + m && y < x + n;
+}
+
+// The batch and tables of a call that moves rows.
+pkv_status move_checks(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                       const int32_t* context_lens, int32_t batch, int32_t mbs,
+                       const pkv_cache_desc* desc) {
+  if (!k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4))
+    return PKV_ERR_INVALID_ARG;
+  if ((int64_t)batch * mbs >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)mbs * kPageSize >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)batch * desc->num_kv_heads >= ((int64_t)1 << 27)) return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+int32_t row_bytes(const pkv_cache_desc* d) {
+  return d->head_dim * (is_fp8(d->cache_dtype) ? 1 : 2);
+}
+
 pkv_status append_checks(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,
                          const int64_t* slot_mapping, const void* k, const void* v,
                          int32_t num_tokens, pkv_dtype kv_dtype) {
@@ -311,13 +350,15 @@ pkv_status decode_validate(const pkv_cache_desc* desc, const void* q, const void
 
 namespace {
 
-// What the biased and shared-prefix forms of the single-token kernel add.
+// What the other forms of the single-token kernel add.
 struct DecodeForm {
   int mode = pkv::kModePlain;
   float softcap = 0.f;
   const float* slopes = nullptr;
   const int32_t* prefix_blocks = nullptr;
   int32_t npb = 0;
+  float* scores = nullptr;
+  float* lse = nullptr;
 };
 
 pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_cache,
@@ -375,6 +416,8 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
   l.p.slopes = form.slopes;
   l.p.prefix_blocks = form.prefix_blocks;
   l.p.npb = form.npb;
+  l.p.scores = form.scores;
+  l.p.lse = form.lse;
   l.group = desc->num_q_heads / desc->num_kv_heads;
   // query-token capacity of the kernel: 1, or the smallest of 2, 4, 8 that
   // holds qlen
@@ -384,7 +427,14 @@ pkv_status decode_impl(const pkv_cache_desc* desc, const void* q, const void* k_
   l.ctas = w.ctas;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (form.mode == pkv::kModeShared) {
+  if (form.mode == pkv::kModeScored) {
+    switch (l.cache) {
+      case pkv::kCacheF16: e = pkv::launch_decode_scored_f16(l); break;
+      case pkv::kCacheBF16: e = pkv::launch_decode_scored_bf16(l); break;
+      case pkv::kCacheE4M3: e = pkv::launch_decode_scored_e4m3(l); break;
+      default: e = pkv::launch_decode_scored_e4m3_tok(l); break;
+    }
+  } else if (form.mode == pkv::kModeShared) {
     e = l.cache == pkv::kCacheF16 ? pkv::launch_decode_shared_f16(l)
                                   : pkv::launch_decode_shared_bf16(l);
   } else if (form.mode == pkv::kModeCap) {
@@ -642,6 +692,226 @@ pkv_status pkv_paged_decode_attention_biased(
                      max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype, out_dtype,
                      workspace, workspace_bytes, stream, /*early_prologue=*/0, 1, window, sinks,
                      nullptr, nullptr, PKV_BF16, 0, form);
+}
+
+size_t pkv_scored_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                  int32_t max_blocks_per_seq, int32_t max_context_len_hint) {
+  const size_t own =
+      pkv_decode_workspace_bytes(desc, batch, max_blocks_per_seq, max_context_len_hint);
+  return own == 0 ? 0 : scored_layout(desc, batch, max_blocks_per_seq).total + own;
+}
+
+pkv_status pkv_paged_decode_attention_scored(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, float* weights, float decay,
+    int32_t batch, int32_t max_blocks_per_seq, int32_t max_context_len_hint, float scale,
+    void* out, pkv_dtype q_dtype, pkv_dtype out_dtype, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if (!(decay >= 0.f && decay <= 1.f)) return PKV_ERR_INVALID_ARG;
+  if (batch > 0 && (!weights || !aligned(weights, 4))) return PKV_ERR_INVALID_ARG;
+  if (batch < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+  const ScoredLayout s = scored_layout(desc, batch, max_blocks_per_seq);
+  char* ws = static_cast<char*>(workspace);
+  char* own = ws != nullptr && workspace_bytes > s.total ? ws + s.total : nullptr;
+  const size_t own_bytes = own != nullptr ? workspace_bytes - s.total : 0;
+  DecodeForm form;
+  form.mode = pkv::kModeScored;
+  form.lse = reinterpret_cast<float*>(ws);
+  form.scores = reinterpret_cast<float*>(ws + s.scores);
+  // the weights kernel may be launched while the decode kernel runs
+  st = decode_impl(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
+                   max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype, out_dtype, own,
+                   own_bytes, stream, /*early_prologue=*/0, 1, 0, 0, nullptr, nullptr, PKV_BF16,
+                   /*trigger_next=*/1, form);
+  if (st != PKV_OK || batch == 0) return st;
+  pkv::WeightParams w;
+  w.scores = form.scores;
+  w.lse = form.lse;
+  w.block_tables = block_tables;
+  w.context_lens = context_lens;
+  w.weights = weights;
+  w.B = batch;
+  w.Hkv = desc->num_kv_heads;
+  w.NB = desc->num_blocks;
+  w.MBS = max_blocks_per_seq;
+  w.decay = decay;
+  // about eight CTAs per SM, none with less than one row per thread
+  const int64_t segs = (int64_t)batch * desc->num_kv_heads;
+  const int64_t most = ((int64_t)max_blocks_per_seq * kPageSize + 255) / 256;
+  int64_t splits = ((int64_t)sm_count_current_device() * 8 + segs - 1) / segs;
+  if (splits > most) splits = most;
+  w.splits = (int32_t)(splits < 1 ? 1 : splits);
+  return pkv::launch_weights(w, desc->num_q_heads / desc->num_kv_heads,
+                             reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
+size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t batch, int32_t max_q_len,
+                                int32_t max_blocks_per_seq) {
+  if (check_desc(desc) != PKV_OK || is_fp8(desc->cache_dtype)) return 0;
+  if (batch <= 0 || max_q_len <= 0 || max_q_len > PKV_MAX_TREE || max_blocks_per_seq <= 0)
+    return 0;
+  return 256;
+}
+
+pkv_status pkv_paged_tree_attention(
+    const pkv_cache_desc* desc, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_start,
+    int32_t batch, int32_t total_q, int32_t max_q_len, const int64_t* tree_mask,
+    int32_t max_blocks_per_seq, float scale, void* out, pkv_dtype q_dtype, pkv_dtype out_dtype,
+    void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || total_q < 0 || max_q_len < 0 || max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (!(scale > 0.f && scale < INFINITY)) return PKV_ERR_INVALID_ARG;  // maxima are unscaled
+  if (is_fp8(desc->cache_dtype) || max_q_len > PKV_MAX_TREE) return PKV_ERR_UNSUPPORTED;
+  if (batch == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !q_start || !tree_mask ||
+      !out)
+    return PKV_ERR_INVALID_ARG;
+  if (q_dtype != desc->cache_dtype) return PKV_ERR_INVALID_ARG;
+  if (out_dtype != PKV_F16 && out_dtype != PKV_BF16 && out_dtype != PKV_F32)
+    return PKV_ERR_UNSUPPORTED;
+  if (batch > 4096) return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)batch * max_blocks_per_seq >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)max_blocks_per_seq * kPageSize >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)total_q * desc->num_q_heads >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(q_start, 4) ||
+      !aligned(tree_mask, 8))
+    return PKV_ERR_INVALID_ARG;
+  const size_t need = pkv_tree_workspace_bytes(desc, batch, max_q_len, max_blocks_per_seq);
+  if (need == 0) return PKV_ERR_CUDA;
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
+    return PKV_ERR_WORKSPACE;
+  pkv::TreeLaunch l;
+  l.p.q = q;
+  l.p.k_cache = k_cache;
+  l.p.v_cache = v_cache;
+  l.p.block_tables = block_tables;
+  l.p.context_lens = context_lens;
+  l.p.q_start = q_start;
+  l.p.tree_mask = tree_mask;
+  l.p.out = out;
+  l.p.err_word = desc->err_word;
+  l.p.B = batch;
+  l.p.Hq = desc->num_q_heads;
+  l.p.Hkv = desc->num_kv_heads;
+  l.p.d = desc->head_dim;
+  l.p.NB = desc->num_blocks;
+  l.p.MBS = max_blocks_per_seq;
+  l.p.total_q = total_q;
+  l.p.max_q = max_q_len;
+  l.p.out_dtype = out_dtype;
+  l.p.scale_log2 = scale * 1.4426950408889634f;
+  l.bf16 = desc->cache_dtype == PKV_BF16;
+  l.stream = reinterpret_cast<cudaStream_t>(stream);
+  return pkv::launch_tree(l) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_accept_path(const pkv_cache_desc* desc, void* k_cache, void* v_cache,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              const int32_t* q_start, const int32_t* path,
+                              const int32_t* path_lens, int32_t max_path, int32_t batch,
+                              int32_t max_blocks_per_seq, int32_t* new_context_lens,
+                              pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || max_path < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+  if (max_path > PKV_MAX_TREE) return PKV_ERR_UNSUPPORTED;
+  if (batch == 0) return PKV_OK;
+  if (!q_start || !path_lens || (!path && max_path > 0)) return PKV_ERR_INVALID_ARG;
+  if (!aligned(q_start, 4) || !aligned(path, 4) || !aligned(path_lens, 4) ||
+      !aligned(new_context_lens, 4))
+    return PKV_ERR_INVALID_ARG;
+  st = move_checks(k_cache, v_cache, block_tables, context_lens, batch, max_blocks_per_seq, desc);
+  if (st != PKV_OK) return st;
+  const size_t nb = (size_t)batch * 4;
+  if (overlap(new_context_lens, nb, context_lens, nb) ||
+      overlap(new_context_lens, nb, q_start, nb + 4) ||
+      overlap(new_context_lens, nb, path_lens, nb) ||
+      overlap(new_context_lens, nb, path, nb * max_path) ||
+      overlap(new_context_lens, nb, block_tables, nb * max_blocks_per_seq))
+    return PKV_ERR_INVALID_ARG;
+  pkv::AcceptParams p;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.scales = nullptr;
+  if (desc->cache_dtype == PKV_FP8_E4M3_TOKEN) p.scales = const_cast<float*>(desc->k_scale);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.q_start = q_start;
+  p.path = path;
+  p.path_lens = path_lens;
+  p.new_lens = new_context_lens;
+  p.err_word = desc->err_word;
+  p.B = batch;
+  p.Hkv = desc->num_kv_heads;
+  p.NB = desc->num_blocks;
+  p.MBS = max_blocks_per_seq;
+  p.max_path = max_path;
+  p.row_bytes = row_bytes(desc);
+  return pkv::launch_accept_path(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_evict(const pkv_cache_desc* desc, void* k_cache, void* v_cache, float* weights,
+                        int32_t* positions, const int32_t* block_tables,
+                        const int32_t* context_lens, const int32_t* old_lens,
+                        const int32_t* num_tokens, int32_t batch, int32_t max_blocks_per_seq,
+                        int32_t budget, int32_t sinks, int32_t recent,
+                        int32_t* new_context_lens, pkv_stream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+  if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return PKV_ERR_INVALID_ARG;
+  if (batch == 0) return PKV_OK;
+  if (!weights || !positions || !old_lens || !num_tokens || !new_context_lens)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(weights, 4) || !aligned(positions, 4) || !aligned(old_lens, 4) ||
+      !aligned(num_tokens, 4) || !aligned(new_context_lens, 4))
+    return PKV_ERR_INVALID_ARG;
+  st = move_checks(k_cache, v_cache, block_tables, context_lens, batch, max_blocks_per_seq, desc);
+  if (st != PKV_OK) return st;
+  if (!pkv::evict_fits(max_blocks_per_seq)) return PKV_ERR_UNSUPPORTED;
+  const size_t nb = (size_t)batch * 4;
+  if (overlap(new_context_lens, nb, context_lens, nb) ||
+      overlap(new_context_lens, nb, old_lens, nb) ||
+      overlap(new_context_lens, nb, num_tokens, nb) ||
+      overlap(new_context_lens, nb, block_tables, nb * max_blocks_per_seq))
+    return PKV_ERR_INVALID_ARG;
+  const int sms = sm_count_current_device();
+  if (sms <= 0) return PKV_ERR_CUDA;
+  pkv::EvictParams p;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.scales = nullptr;
+  if (desc->cache_dtype == PKV_FP8_E4M3_TOKEN) p.scales = const_cast<float*>(desc->k_scale);
+  p.weights = weights;
+  p.positions = positions;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.old_lens = old_lens;
+  p.num_tokens = num_tokens;
+  p.new_lens = new_context_lens;
+  p.err_word = desc->err_word;
+  p.B = batch;
+  p.Hkv = desc->num_kv_heads;
+  p.NB = desc->num_blocks;
+  p.MBS = max_blocks_per_seq;
+  p.budget = budget;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.row_bytes = row_bytes(desc);
+  return pkv::launch_evict(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
 }
 
 size_t pkv_shared_prefix_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,

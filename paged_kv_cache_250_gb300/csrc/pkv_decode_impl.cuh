@@ -149,7 +149,8 @@ __device__ __forceinline__ void store_out_rt(pkv_dtype t, void* base, int64_t id
 // next one's scores apart, 64 sequences of up to 8192 tokens in an E4M3 cache
 // under a window of 4096 took 116.6 us, now 109.7 with both, 105.2 with the bias
 // alone (the plain kernel: 99.8).  kModeShared reads a prefix that all sequences
-// share through its own table.
+// share through its own table.  kModeScored leaves every score, and each row's
+// log of its sum, for the kernel that adds up the rows' weights (pkv_scored.cu).
 template <int D, int G, int QC, int CACHE, bool QBF16, bool DEEP, int MODE>
 __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCtasPerSm)
     decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   static_assert(NC <= 8, "one MMA column per (query token, head)");
   constexpr bool kBiased = MODE == kModeDist || MODE == kModeCap;
   constexpr bool kShared = MODE == kModeShared;
+  constexpr bool kScored = MODE == kModeScored;
   static_assert(MODE == kModePlain || QC == 1, "built for one query token");
   using C = DecodeCfg<D, CACHE, DEEP>;
   constexpr bool kBF = (CACHE == kCacheBF16);  // mma operand type (else fp16)
@@ -526,6 +528,7 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // C-fragment columns 2 c4 and 2 c4 + 1
   float c2a = 0.f, c2b = 0.f;
   float sla = 0.f, slb = 0.f;  // biased: the same two columns' slopes, log2 units
+  float* seg_scores = nullptr;  // scored: the scores of the current segment
 
   auto reset_state = [&]() {
 #pragma unroll
@@ -692,7 +695,8 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // softmax update over all their tokens (log2 domain; tokens past the
   // context are masked), then P.V.  Several pages give the warp independent
   // MMA chains and fewer reductions per token.
-  // rels (biased): the distance of each page's first token from the query.
+  // rels (biased): the distance of each page's first token from the query;
+  // (scored): each page's first token.
   auto compute_pages = [&](auto npc, const uint32_t* kt, const int* valids, const int* rels) {
     constexpr int NP = decltype(npc)::value;
     float x[NP][4];
@@ -765,6 +769,18 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
           if (r8 < w1 && r8 >= sr) x[i][1] = -INFINITY;
           if (r8 + 8 < w0 && r8 + 8 >= sr) x[i][2] = -INFINITY;
           if (r8 + 8 < w1 && r8 + 8 >= sr) x[i][3] = -INFINITY;
+        }
+      }
+      if constexpr (kScored) {  // a token's G scores lie together: 16 G floats a page
+        float* s = seg_scores + ((int64_t)rels[i] + r8) * G + 2 * c4;
+        if constexpr (G == 1) {
+          if (c4 == 0) {
+            s[0] = x[i][0];
+            s[8] = x[i][2];
+          }
+        } else if (2 * c4 < G) {
+          *reinterpret_cast<float2*>(s) = make_float2(x[i][0], x[i][1]);
+          *reinterpret_cast<float2*>(s + 8 * G) = make_float2(x[i][2], x[i][3]);
         }
       }
       mx0 = fmaxf(mx0, fmaxf(x[i][0], x[i][2]));
@@ -902,6 +918,10 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   // a partial with something in it; beside the plain form a NaN sum counts too,
   // so that a NaN a row sees shows in its output however the row was cut
   auto filled = [](float l) -> bool { return MODE == kModePlain ? l > 0.f : l != 0.f; };
+  // the log of a row's sum; a row that saw nothing gives every weight zero
+  [[maybe_unused]] auto lse_of = [](float m, float l) -> float {
+    return l == 0.f ? INFINITY : m + log2f(l);
+  };
   auto merge_cols = [&](int seg, int t, int T) {
     const int b = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;
     const int64_t np = pfx[b + 1] - pfx[b];
@@ -969,6 +989,9 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
         }
       }
       const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+      if constexpr (kScored) {
+        if (col % (D / 4) == 0) p.lse[col_row(b, h, head)] = lse_of(M, lsum);
+      }
       const int64_t ob = col_row(b, h, head) * D + (col % (D / 4)) * 4;
       store_out_rt(p.out_dtype, p.out, ob + 0, acc.x * inv);
       store_out_rt(p.out_dtype, p.out, ob + 1, acc.y * inv);
@@ -1063,6 +1086,10 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       const float i0 = lt0 > 0.f ? vs / lt0 : 0.f;
       const float i1 = lt1 > 0.f ? vs / lt1 : 0.f;
       const bool w0 = col_real(h0), w1 = col_real(h1);
+      if constexpr (kScored) {
+        if (r8 == 0 && w0) p.lse[col_row(b, h, h0)] = lse_of(m2[0], lt0);
+        if (r8 == 0 && w1) p.lse[col_row(b, h, h1)] = lse_of(m2[1], lt1);
+      }
       const int64_t ob0 = (w0 ? col_row(b, h, h0) : 0) * D;
       const int64_t ob1 = (w1 ? col_row(b, h, h1) : 0) * D;
 #pragma unroll
@@ -1209,6 +1236,8 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
         pages_mine = 0;
         have_q = false;
         reset_state();
+        if constexpr (kScored)
+          seg_scores = p.scores + ((int64_t)b * p.Hkv + h) * p.MBS * (kPageSize * G);
         split = x > seg_start || seg_end > sh_hi;
       }
       // this warp's ordinals inside [x, pe)
@@ -1216,11 +1245,13 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       const int64_t hi_j = pe - R.x - warp + NW - 1;
       const int j0 = (int)((lo_j > 0 ? lo_j : 0) / NW);
       const int j1 = (int)((hi_j > 0 ? hi_j : 0) / NW);
-      // biased: first token of the page of ordinal j, less the query's position
-      const int rel_u0 = kBiased ? (int)((int64_t)R.x + warp - seg_start) : 0;
+      // biased: first token of the page of ordinal j, less the query's position;
+      // scored: that token
+      const int rel_u0 = kBiased || kScored ? (int)((int64_t)R.x + warp - seg_start) : 0;
       const int rel_gn = kBiased ? gns[b] : 0, rel_gk = kBiased ? gsk[b] : 0;
       const int rel_t = kBiased ? ctxs[b] - 1 : 0;
       auto rel_of = [&](int j) -> int {
+        if constexpr (kScored) return (rel_u0 + NW * j) * kPageSize;
         if constexpr (!kBiased) return 0;
         const int pgu = rel_u0 + NW * j;
         return (pgu < rel_gn ? pgu : pgu + rel_gk) * kPageSize - rel_t;

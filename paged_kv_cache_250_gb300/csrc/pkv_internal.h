@@ -151,10 +151,14 @@ struct DecodeParams {
   // npb pages
   const int32_t* prefix_blocks;
   int32_t npb;
+  // kept scores (MODE kModeScored): [B][Hkv][MBS * P][group] in log2 units, and
+  // the logarithm of each row's sum [B][Hq], for the weights
+  float* scores;
+  float* lse;
 };
 // Forms of the single-token kernel: distance bias alone, cap (with a distance
-// bias, of slope zero where none is given), shared prefix.
-constexpr int kModePlain = 0, kModeDist = 1, kModeShared = 2, kModeCap = 3;
+// bias, of slope zero where none is given), shared prefix, scores kept.
+constexpr int kModePlain = 0, kModeDist = 1, kModeShared = 2, kModeCap = 3, kModeScored = 4;
 
 struct DecodeLaunch {
   DecodeParams p;
@@ -231,6 +235,10 @@ cudaError_t launch_decode_cap_f16(const DecodeLaunch& l);
 cudaError_t launch_decode_cap_bf16(const DecodeLaunch& l);
 cudaError_t launch_decode_cap_e4m3(const DecodeLaunch& l);
 cudaError_t launch_decode_cap_e4m3_tok(const DecodeLaunch& l);
+cudaError_t launch_decode_scored_f16(const DecodeLaunch& l);
+cudaError_t launch_decode_scored_bf16(const DecodeLaunch& l);
+cudaError_t launch_decode_scored_e4m3(const DecodeLaunch& l);
+cudaError_t launch_decode_scored_e4m3_tok(const DecodeLaunch& l);
 cudaError_t launch_decode_shared_f16(const DecodeLaunch& l);
 cudaError_t launch_decode_shared_bf16(const DecodeLaunch& l);
 cudaError_t launch_decode_f16(const DecodeLaunch& l);
@@ -363,5 +371,97 @@ struct PrefixLaunch {
   cudaStream_t stream;
 };
 cudaError_t launch_prefix(const PrefixLaunch& l);  // the three kernels
+
+// Launch as a programmatic dependent of the kernel in front: the kernel waits
+// (griddepcontrol.wait) before it touches anything that one may write.
+template <typename... KP, typename... A>
+cudaError_t launch_dependent(void (*kern)(KP...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The weights of a scored decode call (pkv_scored.cu).
+struct WeightParams {
+  const float* scores;           // as DecodeParams
+  const float* lse;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* weights;                // [NB][Hkv][P]
+  int32_t B, Hkv, NB, MBS;
+  int32_t splits;                // CTAs per (sequence, KV head)
+  float decay;
+};
+cudaError_t launch_weights(const WeightParams& p, int group, cudaStream_t stream);
+
+// Attention for a tree of drafted tokens (pkv_tree.cu).
+constexpr int kMaxTree = 64;     // nodes of a tree: a row's mask is one 64-bit word
+struct TreeParams {
+  const void* q;                 // [total_q][Hq][d]
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* q_start;        // [B+1]
+  const int64_t* tree_mask;      // [total_q]
+  void* out;
+  int32_t* err_word;
+  int32_t B, Hq, Hkv, d, NB, MBS, total_q, max_q;
+  pkv_dtype out_dtype;
+  float scale_log2;
+};
+struct TreeLaunch {
+  TreeParams p;
+  bool bf16;
+  cudaStream_t stream;
+};
+cudaError_t launch_tree(const TreeLaunch& l);
+
+// Acceptance of a path through a tree (pkv_accept.cu).
+constexpr int kMaxPath = kMaxTree;
+struct AcceptParams {
+  void* k_cache;
+  void* v_cache;
+  float* scales;                 // E4M3 per token: the scale pool (NULL otherwise)
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* q_start;
+  const int32_t* path;           // [B][max_path]
+  const int32_t* path_lens;
+  int32_t* new_lens;             // [B] or NULL
+  int32_t* err_word;
+  int32_t B, Hkv, NB, MBS, max_path;
+  int32_t row_bytes;             // of one K (or V) row of one KV head
+};
+cudaError_t launch_accept_path(const AcceptParams& p, cudaStream_t stream);
+
+// Eviction by accumulated weight (pkv_evict.cu).
+struct EvictParams {
+  void* k_cache;
+  void* v_cache;
+  float* scales;                 // E4M3 per token: the scale pool (NULL otherwise)
+  float* weights;                // [NB][Hkv][P]
+  int32_t* positions;            // [NB][Hkv][P]
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* old_lens;
+  const int32_t* num_tokens;
+  int32_t* new_lens;             // [B]
+  int32_t* err_word;
+  int32_t B, Hkv, NB, MBS;
+  int32_t budget, sinks, recent;
+  int32_t row_bytes;
+};
+bool evict_fits(int32_t max_blocks_per_seq);
+cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);
 
 }  // namespace pkv
