@@ -12,6 +12,7 @@
 #include "pkv.h"
 #include "pkv_internal.h"
 #include "pkv_prefix_line.h"
+#include "pkv_tree_line.h"
 
 static_assert(PKV_MAX_TREE == pkv::kMaxTree && PKV_MAX_TREE == pkv::kMaxPath, "one limit");
 
@@ -256,6 +257,19 @@ ScoredLayout scored_layout(const pkv_cache_desc* d, int32_t batch, int32_t mbs) 
   s.scores = align256(rows * sizeof(float));
   s.total = align256(s.scores + rows * mbs * kPageSize * sizeof(float));
   return s;
+}
+
+// Tree attention: two partial slots of 256 rows per CTA, whatever the batch.
+struct TreeLayout {
+  size_t ml, o, total;
+};
+TreeLayout tree_layout(const pkv_cache_desc* d, int sms) {
+  const size_t rows = (size_t)sms * 2 * 2 * pkv::kTreeRows;
+  TreeLayout t;
+  t.ml = align256((size_t)sms * sizeof(int4));
+  t.o = align256(t.ml + rows * sizeof(float2));
+  t.total = align256(t.o + rows * d->head_dim * sizeof(float));
+  return t;
 }
 
 // Whether [a, a + n) and [b, b + m) share a byte (null: no).
@@ -754,7 +768,8 @@ size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t batch, int32
   if (check_desc(desc) != PKV_OK || is_fp8(desc->cache_dtype)) return 0;
   if (batch <= 0 || max_q_len <= 0 || max_q_len > PKV_MAX_TREE || max_blocks_per_seq <= 0)
     return 0;
-  return 256;
+  const int sms = sm_count_current_device();
+  return sms <= 0 ? 0 : tree_layout(desc, sms).total;
 }
 
 pkv_status pkv_paged_tree_attention(
@@ -776,7 +791,7 @@ pkv_status pkv_paged_tree_attention(
   if (q_dtype != desc->cache_dtype) return PKV_ERR_INVALID_ARG;
   if (out_dtype != PKV_F16 && out_dtype != PKV_BF16 && out_dtype != PKV_F32)
     return PKV_ERR_UNSUPPORTED;
-  if (batch > 4096) return PKV_ERR_UNSUPPORTED;
+  if (batch > pkv::kTreeMaxBatch) return PKV_ERR_UNSUPPORTED;
   if ((int64_t)batch * max_blocks_per_seq >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
   if ((int64_t)max_blocks_per_seq * kPageSize >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
   if ((int64_t)total_q * desc->num_q_heads >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;
@@ -784,31 +799,45 @@ pkv_status pkv_paged_tree_attention(
       !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(q_start, 4) ||
       !aligned(tree_mask, 8))
     return PKV_ERR_INVALID_ARG;
-  const size_t need = pkv_tree_workspace_bytes(desc, batch, max_q_len, max_blocks_per_seq);
-  if (need == 0) return PKV_ERR_CUDA;
-  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
+  const int sms = sm_count_current_device();
+  if (sms <= 0) return PKV_ERR_CUDA;
+  const TreeLayout t = tree_layout(desc, sms);
+  if (workspace == nullptr || workspace_bytes < t.total || !aligned(workspace, 256))
     return PKV_ERR_WORKSPACE;
   pkv::TreeLaunch l;
-  l.p.q = q;
-  l.p.k_cache = k_cache;
-  l.p.v_cache = v_cache;
+  st = encode_cache_map(&l.tmap_k, k_cache, desc);
+  if (st != PKV_OK) return st;
+  st = encode_cache_map(&l.tmap_v, v_cache, desc);
+  if (st != PKV_OK) return st;
+  st = encode_q_map(&l.tmap_q, q, desc, total_q);
+  if (st != PKV_OK) return st;
+  char* ws = static_cast<char*>(workspace);
   l.p.block_tables = block_tables;
   l.p.context_lens = context_lens;
   l.p.q_start = q_start;
   l.p.tree_mask = tree_mask;
   l.p.out = out;
+  l.p.meta = reinterpret_cast<int4*>(ws);
+  l.p.part_ml = reinterpret_cast<float2*>(ws + t.ml);
+  l.p.part_o = reinterpret_cast<float*>(ws + t.o);
   l.p.err_word = desc->err_word;
   l.p.B = batch;
   l.p.Hq = desc->num_q_heads;
   l.p.Hkv = desc->num_kv_heads;
-  l.p.d = desc->head_dim;
   l.p.NB = desc->num_blocks;
   l.p.MBS = max_blocks_per_seq;
   l.p.total_q = total_q;
   l.p.max_q = max_q_len;
+  // as many CTAs as the longest sequences the arguments allow would keep busy
+  const int rows = max_q_len * (desc->num_q_heads / desc->num_kv_heads);
+  l.p.ctas = (int32_t)pkv::tree_shares(
+      batch * pkv::tree_seq_cost(desc->num_kv_heads, rows,
+                                 pkv::tree_blocks(max_blocks_per_seq * kPageSize)),
+      sms);
   l.p.out_dtype = out_dtype;
   l.p.scale_log2 = scale * 1.4426950408889634f;
   l.bf16 = desc->cache_dtype == PKV_BF16;
+  l.d = desc->head_dim;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
   return pkv::launch_tree(l) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -406,25 +406,32 @@ cudaError_t launch_weights(const WeightParams& p, int group, cudaStream_t stream
 // Attention for a tree of drafted tokens (pkv_tree.cu).
 constexpr int kMaxTree = 64;     // nodes of a tree: a row's mask is one 64-bit word
 struct TreeParams {
-  const void* q;                 // [total_q][Hq][d]
-  const void* k_cache;
-  const void* v_cache;
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* q_start;        // [B+1]
   const int64_t* tree_mask;      // [total_q]
-  void* out;
+  void* out;                     // [total_q][Hq][d]
+  // Partials: CTA c's part of a segment that began before it in slot 2 c, of one
+  // that begins in it and goes on in 2 c + 1: [slot][256 rows].
+  float2* part_ml;               // (m in log2 units, l)
+  float* part_o;                 // [d] each, unnormalised
+  int4* meta;                    // [ctas] what each CTA left, for the merge
   int32_t* err_word;
-  int32_t B, Hq, Hkv, d, NB, MBS, total_q, max_q;
+  int32_t B, Hq, Hkv, NB, MBS, total_q, max_q;
+  int32_t ctas;
   pkv_dtype out_dtype;
   float scale_log2;
 };
 struct TreeLaunch {
   TreeParams p;
+  CUtensorMap tmap_q;            // as the prefill kernel's
+  CUtensorMap tmap_k;
+  CUtensorMap tmap_v;
   bool bf16;
+  int32_t d;
   cudaStream_t stream;
 };
-cudaError_t launch_tree(const TreeLaunch& l);
+cudaError_t launch_tree(const TreeLaunch& l);  // both kernels
 
 // Acceptance of a path through a tree (pkv_accept.cu).
 constexpr int kMaxPath = kMaxTree;
