@@ -332,8 +332,8 @@ PKV_API size_t pkv_scored_workspace_bytes(const pkv_cache_desc* desc, int32_t ba
  * sum, so a row need not be cleared when it is appended; with decay 0 every
  * position's is, whatever was there (the first call after a prompt).
  *   weights       device fp32 [num_blocks][num_kv_heads][page_size], beside the
- *                 caches: the weight of the row in the same block and slot.
- *                 Entries of positions the call does not see stay as they are.
+ *                 caches: the weight of the row in the same block and slot;
+ *                 16-byte aligned.  Entries of positions the call does not see stay as they are.
  *   decay         0 .. 1: 1 sums over all steps, less forgets older ones.
  *   workspace     of at least pkv_scored_workspace_bytes() bytes.
  * A block that two sequences of the call share gets the sum of one of them, or
@@ -431,7 +431,8 @@ PKV_API pkv_status pkv_kv_accept_path(
  * row belongs to.  A sequence of at most `budget` rows keeps them all.
  *   weights       as for pkv_paged_decode_attention_scored.
  *   positions     device int32 [num_blocks][num_kv_heads][page_size]: the token
- *                 (0, 1, ...) of the row in the same block and slot.
+ *                 (0, 1, ...) of the row in the same block and slot; 16-byte
+ *                 aligned.
  *   context_lens  device int32 [batch], rows cached now.
  *   old_lens      device int32 [batch], the rows whose positions are known: the
  *                 new_context_lens of the sequence's last call, or 0 before the
@@ -448,7 +449,7 @@ PKV_API pkv_status pkv_kv_accept_path(
  * is, its entry of new_context_lens too.  A table entry outside the pool is
  * PKV_ERR_BOUNDS: its rows are the first to go and are never read or written.
  * Blocks must belong to one sequence of the call (copy shared ones first:
- * pkv_copy_blocks).  Tables of up to 24576 blocks per sequence (more returns
+ * pkv_copy_blocks).  Tables of up to 49152 blocks per sequence (more returns
  * PKV_ERR_UNSUPPORTED).  All cache types; no workspace. */
 PKV_API pkv_status pkv_kv_evict(
     const pkv_cache_desc* desc, void* k_cache, void* v_cache, float* weights,

@@ -724,7 +724,7 @@ pkv_status pkv_paged_decode_attention_scored(
   pkv_status st = check_desc(desc);
   if (st != PKV_OK) return st;
   if (!(decay >= 0.f && decay <= 1.f)) return PKV_ERR_INVALID_ARG;
-  if (batch > 0 && (!weights || !aligned(weights, 4))) return PKV_ERR_INVALID_ARG;
+  if (batch > 0 && (!weights || !aligned(weights, 16))) return PKV_ERR_INVALID_ARG;
   if (batch < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
   const ScoredLayout s = scored_layout(desc, batch, max_blocks_per_seq);
   char* ws = static_cast<char*>(workspace);
@@ -903,7 +903,7 @@ pkv_status pkv_kv_evict(const pkv_cache_desc* desc, void* k_cache, void* v_cache
   if (batch == 0) return PKV_OK;
   if (!weights || !positions || !old_lens || !num_tokens || !new_context_lens)
     return PKV_ERR_INVALID_ARG;
-  if (!aligned(weights, 4) || !aligned(positions, 4) || !aligned(old_lens, 4) ||
+  if (!aligned(weights, 16) || !aligned(positions, 16) || !aligned(old_lens, 4) ||
       !aligned(num_tokens, 4) || !aligned(new_context_lens, 4))
     return PKV_ERR_INVALID_ARG;
   st = move_checks(k_cache, v_cache, block_tables, context_lens, batch, max_blocks_per_seq, desc);

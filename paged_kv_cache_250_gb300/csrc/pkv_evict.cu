@@ -5,7 +5,7 @@
 // positions and the most recent ones) above all others, those by weight (the
 // float's bits, mapped so that they order as unsigned numbers; NaN above
 // infinity), rows of a page outside the pool below all.  The budget-th largest
-// key T is found digit by digit (11, 11 and 10 bits) from histograms; kept are
+// key T is found digit by digit (8 bits each) from histograms; kept are
 // the keys above T and, of those equal to T, the first by index, as many as
 // the budget leaves.
 //
@@ -16,8 +16,7 @@
 //
 // One cluster of CL CTAs per (sequence, KV head), each with a contiguous slice
 // of the rows: the keys stay in shared memory, a warp takes a contiguous stretch
-// of them, so counts before a row are those of the CTAs and warps before plus a
-// ballot.  Histograms, counts and the two lists cross CTAs through distributed
+// of them, so counts before a row are those of the CTAs, warps and lanes before.  Histograms, counts and the two lists cross CTAs through distributed
 // shared memory; CTA r then moves the pairs r, r + CL, ...
 #include <cooperative_groups.h>
 
@@ -31,10 +30,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kBins = 2048;  // of a digit
+constexpr int kBins = 256, kDigits = 4;
 constexpr uint32_t kGuarded = 0xffffffffu, kNan = 0xfffffffeu;
-constexpr size_t kFixedSmem = 3 * kBins * 4 + 2 * kWarps * 4 + 32;
+constexpr int kMaxWarps = 32;
+constexpr size_t kFixedSmem = kDigits * kBins * 4 + 2 * kMaxWarps * 4 + 32;
 constexpr size_t kSmemLimit = 227 * 1024;
 
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -48,17 +47,19 @@ __host__ __device__ constexpr int64_t slice_rows(int64_t rows, int cl) {
   return (rows + 32 * cl - 1) / (32 * cl) * 32;
 }
 constexpr size_t smem_of(int64_t rows, int cl) {
-  return kFixedSmem + slice_rows(rows, cl) * 4 + slice_rows(rows, cl) / 8;
+  return kFixedSmem + slice_rows(rows, cl) * 4 + slice_rows(rows, cl) / 4 +
+         slice_rows(rows, cl) / kPageSize * 4;
 }
 
-template <int CL>
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
+template <int CL, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams p) {
+  constexpr int NW = NT / 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ uint32_t smem[];
-  uint32_t* hist = smem;                // [3][kBins]
-  uint32_t* warp_a = hist + 3 * kBins;  // [kWarps] counts of the warps
-  uint32_t* warp_b = warp_a + kWarps;
-  uint32_t* pick = warp_b + kWarps;     // [4] digit, count above it, count in it
+  extern __shared__ __align__(16) uint32_t smem[];
+  uint32_t* hist = smem;                       // [kDigits][kBins]
+  uint32_t* warp_a = hist + kDigits * kBins;   // [NW] counts of the warps
+  uint32_t* warp_b = warp_a + kMaxWarps;
+  uint32_t* pick = warp_b + kMaxWarps;  // [4] digit, count above it, count in it
   uint32_t* tot = pick + 4;             // [3] this CTA's ties, holes, late rows
   uint32_t* keys = tot + 4;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     if constexpr (CL > 1) return cg::this_cluster().map_shared_rank(x, r);
     else return x;
   };
-  for (int i = tid; i < 3 * kBins; i += kThreads) hist[i] = 0;
+  for (int i = tid; i < kDigits * kBins; i += NT) hist[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = p.context_lens[b], old = p.old_lens[b], told = p.num_tokens[b];
   if (n < 0 || n > p.MBS * kPageSize || old < 0 || old > n || told < n) {
@@ -83,60 +84,91 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
   const int slice = (int)slice_rows(n, CL);
   const int lo = (int)min((int64_t)n, (int64_t)rank * slice);
   const int cnt = min(slice, n - lo);          // rows lo .. lo + cnt - 1
-  uint32_t* bits = keys + slice;               // a bit per row: kept
+  int* rows = reinterpret_cast<int*>(keys + slice);  // first row of each page, or -1
+  uint8_t* nibs = reinterpret_cast<uint8_t*>(rows + slice / kPageSize);  // see below, four rows each
   const int32_t* table = p.block_tables + (int64_t)b * p.MBS;
-  auto row_of = [&](int u) -> int64_t {  // of the pool, or -1
+  auto row_of = [&](int u) -> int {  // of the pool, or -1
     const int blk = table[u / kPageSize];
     if (blk < 0 || blk >= p.NB) return -1;
-    return ((int64_t)blk * p.Hkv + h) * kPageSize + u % kPageSize;
+    return (blk * p.Hkv + h) * kPageSize + u % kPageSize;  // the pool has less than 2^31 rows
   };
+  for (int i = tid; i < (cnt + kPageSize - 1) / kPageSize; i += NT) {
+    rows[i] = row_of(lo + i * kPageSize);  // a slice is whole pages
+    if (rows[i] < 0) report_error(p.err_word, PKV_ERR_BOUNDS);
+  }
   __syncthreads();
 
-  // ---- keys, and the positions of the rows that came since the last call
-  for (int i = tid; i < cnt; i += kThreads) {
-    const int u = lo + i;
-    const int64_t row = row_of(u);
-    uint32_t key = 0;
-    if (row < 0) {
-      report_error(p.err_word, PKV_ERR_BOUNDS);
-    } else {
-      const int pos = u >= old ? told - n + u : p.positions[row];
-      if (u >= old) p.positions[row] = pos;
-      key = pos < p.sinks || pos >= told - p.recent ? kGuarded : key_of(p.weights[row]);
+  // ---- keys, and the positions of the rows that came since the last call; a
+  // thread takes four rows of a page at a time, kAhead of them in flight
+  constexpr int kAhead = 4;
+  for (int i0 = 4 * tid; i0 < cnt; i0 += 4 * NT * kAhead) {
+    float4 wq[kAhead];
+    int4 pq[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + 4 * NT * a;
+      if (i >= cnt) break;
+      const int row = rows[i / kPageSize] + i % kPageSize;
+      const bool in = rows[i / kPageSize] >= 0;
+      if (in && n > p.budget) wq[a] = *reinterpret_cast<const float4*>(p.weights + row);
+      if (in && lo + i < old) pq[a] = *reinterpret_cast<const int4*>(p.positions + row);
     }
-    if (n > p.budget) {
-      keys[i] = key;
-      atomicAdd(&hist[key >> 21], 1u);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + 4 * NT * a, u = lo + i;
+      if (i >= cnt) break;
+      const int row = rows[i / kPageSize] + i % kPageSize;
+      const bool in = rows[i / kPageSize] >= 0;
+      const float wv[4] = {wq[a].x, wq[a].y, wq[a].z, wq[a].w};
+      int pv[4] = {pq[a].x, pq[a].y, pq[a].z, pq[a].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (u + e >= old) pv[e] = told - n + u + e;
+      if (in && u >= old && i + 4 <= cnt) {
+        *reinterpret_cast<int4*>(p.positions + row) = make_int4(pv[0], pv[1], pv[2], pv[3]);
+      } else if (in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (u + e >= old && i + e < cnt) p.positions[row + e] = pv[e];
+      }
+      if (n <= p.budget) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i + e >= cnt) break;
+        uint32_t key = 0;
+        if (in) key = pv[e] < p.sinks || pv[e] >= told - p.recent ? kGuarded : key_of(wv[e]);
+        keys[i + e] = key;
+        atomicAdd(&hist[key >> 24], 1u);
+      }
     }
   }
   if (n <= p.budget) return;  // the same in every CTA of the cluster
   sync();
 
   // ---- the budget-th largest key
-  uint32_t prefix = 0, need = (uint32_t)p.budget;  // digits so far; rows still to keep
+  uint32_t T = 0, need = (uint32_t)p.budget;  // digits so far; rows still to keep
   uint32_t in_last = 0;
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    uint32_t* hh = hist + (24 - shift) / 8 * kBins;
+    if (shift < 24) {
+      for (int i = 4 * tid; i < cnt; i += 4 * NT) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    uint32_t* hh = hist + pass * kBins;
-    if (pass > 0) {
-      for (int i = tid; i < cnt; i += kThreads) {
-        const uint32_t k = keys[i];
-        if (k >> (pass == 1 ? 21 : 10) == prefix)
-          atomicAdd(&hh[(k >> shift) & (pass == 1 ? 0x7ff : 0x3ff)], 1u);
+        for (int e = 0; e < 4; ++e)
+          if ((k[e] ^ T) >> (shift + 8) == 0 && i + e < cnt)
+            atomicAdd(&hh[(k[e] >> shift) & 0xff], 1u);
       }
       sync();
     }
-    // thread t holds bins 2 t and 2 t + 1 counted from the highest
-    const int top = kBins - 1 - 2 * tid;
-    uint32_t c0 = 0, c1 = 0;
+    // thread t holds bin t counted from the highest
+    uint32_t c = 0;
+    if (tid < kBins) {
 #pragma unroll
-    for (int r = 0; r < CL; ++r) {
-      const uint2 c = *reinterpret_cast<const uint2*>(at_rank(hh, r) + top - 1);
-      c0 += c.y;
-      c1 += c.x;
+      for (int r = 0; r < CL; ++r) c += at_rank(hh, r)[kBins - 1 - tid];
     }
-    uint32_t inc = c0 + c1;
+    uint32_t inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -145,160 +177,211 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     if (lane == 31) warp_a[warp] = inc;
     __syncthreads();
     const uint32_t before =
-        __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0u) + inc - c0 - c1;
-    if (before < need && need <= before + c0 + c1) {  // one thread
-      const bool second = need > before + c0;
-      pick[0] = (uint32_t)(second ? top - 1 : top);
-      pick[1] = second ? before + c0 : before;
-      pick[2] = second ? c1 : c0;
+        __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0u) + inc - c;
+    if (before < need && need <= before + c) {  // one thread
+      pick[0] = (uint32_t)(kBins - 1 - tid);
+      pick[1] = before;
+      pick[2] = c;
     }
     __syncthreads();
-    prefix = prefix << (pass == 2 ? 10 : 11) | pick[0];
+    T |= pick[0] << shift;
     need -= pick[1];
     in_last = pick[2];
+    if (need == in_last) break;  // every row whose key begins with these digits is kept
     __syncthreads();
   }
-  const uint32_t T = prefix;  // `need` of the in_last rows with this key are kept
+  // Kept are the keys above T and `need` of those that equal it.  (Where the
+  // search ended early T is the least key that begins with the digits.)
 
-  // ---- kept rows, holes and late rows
-  const int per = (cnt + 32 * kWarps - 1) / (32 * kWarps) * 32;  // rows of a warp
+  // ---- events: rows below the budget that go (holes), rows behind it that stay
+  // (late rows).  A lane takes four rows of a warp's 128; a nibble says which of
+  // them are events.
+  const int per = (cnt + 128 * NW - 1) / (128 * NW) * 128;  // rows of a warp
   const int w0 = min(cnt, warp * per), w1 = min(cnt, w0 + per);
-  const uint32_t below = (1u << lane) - 1;
+  auto lanes_before = [&](uint32_t v) -> uint32_t {  // sum over the lanes before this one
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x - v;
+  };
+  auto four = [&](int i, uint32_t (&k)[4]) -> uint32_t {  // keys i .. i + 3; those that equal T
+    const uint4 v = i < w1 ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0, 0, 0, 0);
+    k[0] = v.x;
+    k[1] = v.y;
+    k[2] = v.z;
+    k[3] = v.w;
+    uint32_t eq = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) eq |= (i + e < w1 && k[e] == T ? 1u : 0u) << e;
+    return eq;
+  };
+  __syncthreads();
   uint32_t ties = 0;  // rows with key T before this warp's
   if (need < in_last) {
-    for (int i0 = w0; i0 < w1; i0 += 32)
-      ties += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && keys[i0 + lane] == T));
+    uint32_t k[4];
+    for (int i = w0 + 4 * lane; i < w1; i += 128) ties += __popc(four(i, k));
+    ties = __reduce_add_sync(0xffffffffu, ties);
     if (lane == 0) warp_a[warp] = ties;
     __syncthreads();
-    const uint32_t all = __reduce_add_sync(0xffffffffu, warp_a[lane]);
-    ties = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0u);
+    const uint32_t v = lane < NW ? warp_a[lane] : 0u;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, v);
+    ties = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u);
     if (tid == 0) tot[0] = all;
     sync();
     for (int r = 0; r < rank; ++r) ties += *at_rank(tot, r);
   }
-  uint32_t holes = 0, late = 0;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const bool in = i < w1;
-    const uint32_t k = in ? keys[i] : 0u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, in && k == T);
-    const bool keep = in && (k > T || (k == T && ties + __popc(eq & below) < need));
-    if (need < in_last) ties += __popc(eq);
-    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
-    holes += __popc(__ballot_sync(0xffffffffu, in && !keep && lo + i < p.budget));
-    late += __popc(__ballot_sync(0xffffffffu, keep && lo + i >= p.budget));
-    if (lane == 0) bits[i0 >> 5] = kept;
+  uint32_t events = 0, holes = 0;
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    const int i = i0 + 4 * lane, u = lo + i;
+    uint32_t k[4], keep = 0;
+    const uint32_t eq = four(i, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) keep |= (k[e] >= T ? 1u : 0u) << e;
+    if (need < in_last) {  // the first of the equal keys only
+      uint32_t t = ties + lanes_before(__popc(eq));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((eq >> e) & 1)
+          if (t++ >= need) keep &= ~(1u << e);
+      ties += __reduce_add_sync(0xffffffffu, __popc(eq));
+    }
+    const uint32_t in = i >= w1 ? 0u : i + 4 <= w1 ? 15u : (1u << (w1 - i)) - 1;
+    const uint32_t low = u >= p.budget ? 0u : u + 4 <= p.budget ? 15u : (1u << (p.budget - u)) - 1;
+    const uint32_t ev = (keep ^ low) & in;
+    if (in != 0) nibs[i >> 2] = (uint8_t)ev;
+    events += __popc(ev);
+    holes += __popc(ev & low);
   }
+  events = __reduce_add_sync(0xffffffffu, events);
+  holes = __reduce_add_sync(0xffffffffu, holes);
   __syncthreads();  // warp_a is free again
   if (lane == 0) {
-    warp_a[warp] = holes;
-    warp_b[warp] = late;
+    warp_a[warp] = events;
+    warp_b[warp] = holes;
   }
   __syncthreads();
-  const uint32_t hv = warp_a[lane], lv = warp_b[lane];
-  int pairs = (int)__reduce_add_sync(0xffffffffu, hv);
-  uint32_t hole_at = __reduce_add_sync(0xffffffffu, lane < warp ? hv : 0u);
-  uint32_t late_at = __reduce_add_sync(0xffffffffu, lane < warp ? lv : 0u);
+  const uint32_t ev_w = lane < NW ? warp_a[lane] : 0u;
+  uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? ev_w : 0u);  // events before
+  uint32_t pairs = __reduce_add_sync(0xffffffffu, lane < NW ? warp_b[lane] : 0u);
   if constexpr (CL > 1) {
-    const uint32_t lates = __reduce_add_sync(0xffffffffu, lv);
+    const uint32_t all = __reduce_add_sync(0xffffffffu, ev_w);
     if (tid == 0) {
-      tot[1] = (uint32_t)pairs;
-      tot[2] = lates;
+      tot[1] = all;
+      tot[2] = pairs;
     }
     sync();  // and the keys of every CTA are read for the last time
     pairs = 0;
     for (int r = 0; r < CL; ++r) {
-      const uint32_t hr = at_rank(tot, r)[1], lr = at_rank(tot, r)[2];
-      if (r < rank) {
-        hole_at += hr;
-        late_at += lr;
-      }
-      pairs += (int)hr;
+      if (r < rank) at += at_rank(tot, r)[1];
+      pairs += at_rank(tot, r)[2];
     }
   }
 
   // ---- the i-th hole and the i-th late row, over the keys: i / CL in the CTA
-  // i % CL.  There are at most n / 2 pairs, so both lists fit a slice.
+  // i % CL.  In the order of the rows all holes come before all late rows.  There
+  // are at most n / 2 pairs, so both lists fit a slice.
   const int half = slice / 2;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int u = lo + i0 + lane;
-    const bool in = i0 + lane < w1, keep = (bits[i0 >> 5] >> lane) & 1;
-    const bool is_hole = in && !keep && u < p.budget, is_late = keep && u >= p.budget;
-    const uint32_t hb = __ballot_sync(0xffffffffu, is_hole);
-    const uint32_t lb = __ballot_sync(0xffffffffu, is_late);
-    if (is_hole) {
-      const uint32_t i = hole_at + __popc(hb & below);
-      at_rank(keys, (int)(i % CL))[i / CL] = (uint32_t)u;
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const uint32_t ev = i < w1 ? nibs[i >> 2] : 0u;
+    uint32_t o = at + lanes_before(__popc(ev));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (!((ev >> e) & 1)) continue;
+      const uint32_t x = o < pairs ? o : o - pairs;
+      at_rank(keys, (int)(x % CL))[(o < pairs ? 0 : half) + x / CL] = (uint32_t)(lo + i + e);
+      ++o;
     }
-    if (is_late) {
-      const uint32_t i = late_at + __popc(lb & below);
-      at_rank(keys, (int)(i % CL))[half + i / CL] = (uint32_t)u;
-    }
-    hole_at += __popc(hb);
-    late_at += __popc(lb);
+    at += __reduce_add_sync(0xffffffffu, __popc(ev));
   }
   sync();
-  const uint32_t* from = keys + half;
-  const int mine = (pairs - rank + CL - 1) / CL;
+  int* to = reinterpret_cast<int*>(keys);
+  int* from = to + half;
+  const int mine = ((int)pairs - rank + CL - 1) / CL;
 
-  // ---- the moves: a warp takes four pairs at a time, 16 bytes per lane
-  constexpr int kAt = 4;
-  const int cpr = p.row_bytes >> 4;  // pieces of a row: 8 or 16
-  for (int i0 = warp * kAt; i0 < mine; i0 += kWarps * kAt) {
-    // lane 2 i: the hole's row of pair i; lane 2 i + 1: the late row's
-    int64_t row = -1;
-    int at = 0;
-    if (lane < 2 * kAt && i0 + (lane >> 1) < mine) {
-      at = (int)(lane & 1 ? from[i0 + (lane >> 1)] : keys[i0 + (lane >> 1)]);
-      row = row_of(at);
+  // ---- the moves.  The lists become rows of the pool (-1: outside, nothing
+  // moves); a thread takes the small things of a pair, whose loads are in flight
+  // while K and V move.
+  struct Small {
+    int dst = -1, pos;
+    float w, s[2];
+  };
+  auto scale_at = [](int r, int e) -> int64_t {  // a page's 16 K scales, then its 16 V scales
+    return (r / kPageSize * (int64_t)2 + e) * kPageSize + r % kPageSize;
+  };
+  auto small_load = [&](int i, Small& x) {
+    const int u = from[i], src = row_of(u);
+    int dst = row_of(to[i]);
+    if (src < 0) dst = -1;
+    to[i] = dst;
+    from[i] = src;
+    x.dst = dst;
+    if (dst < 0) return;
+    x.w = p.weights[src];
+    x.pos = u >= old ? told - n + u : p.positions[src];
+    if (p.scales != nullptr) {
+      x.s[0] = p.scales[scale_at(src, 0)];
+      x.s[1] = p.scales[scale_at(src, 1)];
     }
-    int64_t to[kAt], src[kAt];
-#pragma unroll
-    for (int i = 0; i < kAt; ++i) {
-      to[i] = __shfl_sync(0xffffffffu, row, 2 * i);
-      src[i] = __shfl_sync(0xffffffffu, row, 2 * i + 1);
+  };
+  auto small_store = [&](const Small& x) {
+    if (x.dst < 0) return;
+    p.weights[x.dst] = x.w;
+    p.positions[x.dst] = x.pos;
+    if (p.scales != nullptr) {
+      p.scales[scale_at(x.dst, 0)] = x.s[0];
+      p.scales[scale_at(x.dst, 1)] = x.s[1];
     }
-    const int late_u = __shfl_down_sync(0xffffffffu, at, 1);
-    const int64_t late_row = __shfl_down_sync(0xffffffffu, row, 1);
-    if (lane < 2 * kAt && !(lane & 1) && row >= 0 && late_row >= 0) {
-      p.weights[row] = p.weights[late_row];
-      p.positions[row] = late_u >= old ? told - n + late_u : p.positions[late_row];
-      if (p.scales != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          auto of = [&](int64_t r) { return (r / kPageSize * 2 + i) * kPageSize + r % kPageSize; };
-          p.scales[of(row)] = p.scales[of(late_row)];
-        }
-      }
+  };
+  Small first;
+  for (int i = tid; i < mine; i += NT) {
+    if (i == tid) {
+      small_load(i, first);
+    } else {
+      Small x;
+      small_load(i, x);
+      small_store(x);
     }
-    uint4 kv[kAt];
-    bool go[kAt];
-    // 16 pieces: half the lanes take K, the others V; 8: the lanes above 16 rest
-    const int which = lane / cpr;
-    const uint4* in = static_cast<const uint4*>(which == 0 ? p.k_cache : p.v_cache);
-    uint4* out = static_cast<uint4*>(which == 0 ? p.k_cache : p.v_cache);
-#pragma unroll
-    for (int i = 0; i < kAt; ++i) {
-      go[i] = which < 2 && to[i] >= 0 && src[i] >= 0;
-      if (go[i]) kv[i] = in[src[i] * cpr + lane % cpr];
-    }
-#pragma unroll
-    for (int i = 0; i < kAt; ++i)
-      if (go[i]) out[to[i] * cpr + lane % cpr] = kv[i];
   }
+  __syncthreads();
+  // K and V: 16 bytes per lane, a row's 2 cpr pieces side by side (a warp holds
+  // one pair, or two of E4M3 and d 64), kAt steps in flight
+  constexpr int kAt = 8;
+  const int cpr = p.row_bytes >> 4;  // pieces of a row: 8 or 16
+  const int wide = 16 / cpr;         // pairs per warp: 1 or 2
+  const int sub = lane / (2 * cpr), piece = lane % (2 * cpr);
+  const bool is_v = piece >= cpr;
+  const uint4* in = static_cast<const uint4*>(is_v ? p.v_cache : p.k_cache) + piece % cpr;
+  uint4* out = static_cast<uint4*>(is_v ? p.v_cache : p.k_cache) + piece % cpr;
+  for (int i0 = warp * wide; i0 < mine; i0 += NW * wide * kAt) {
+    uint4 data[kAt];
+    int dst[kAt];
+#pragma unroll
+    for (int e = 0; e < kAt; ++e) {
+      const int i = i0 + e * NW * wide + sub;
+      dst[e] = i < mine ? to[i] : -1;
+      if (dst[e] >= 0) data[e] = in[(int64_t)from[i] * cpr];
+    }
+#pragma unroll
+    for (int e = 0; e < kAt; ++e)
+      if (dst[e] >= 0) out[(int64_t)dst[e] * cpr] = data[e];
+  }
+  small_store(first);
 }
 
 }  // namespace
 
-constexpr int kMaxCluster = 8;
-constexpr int32_t kMaxBlocks = 24576;  // of a table: what the largest cluster holds
+constexpr int kMaxCluster = 16;  // opt-in: more than the portable 8
+constexpr int32_t kMaxBlocks = 49152;  // of a table: what the largest cluster holds
 bool evict_fits(int32_t mbs) { return mbs <= kMaxBlocks; }
-
 static_assert(smem_of((int64_t)kMaxBlocks * kPageSize, kMaxCluster) <= kSmemLimit, "fits");
 
-template <int CL>
+template <int CL, int NT>
 static cudaError_t launch_cluster(const EvictParams& p, cudaStream_t stream) {
-  auto kern = evict_kernel<CL>;
+  auto kern = evict_kernel<CL, NT>;
   static std::atomic<uint64_t> configured{0};  // a bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -306,12 +389,14 @@ static cudaError_t launch_cluster(const EvictParams& p, cudaStream_t stream) {
   const uint64_t bit = 1ull << (dev & 63);
   if (dev > 63 || !(configured.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+    if (e == cudaSuccess && CL > 8)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.Hkv * CL));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem_of((int64_t)p.MBS * kPageSize, CL);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -326,17 +411,35 @@ static cudaError_t launch_cluster(const EvictParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <int CL>
+static cudaError_t launch_threads(const EvictParams& p, int nt, cudaStream_t stream) {
+  return nt == 1024  ? launch_cluster<CL, 1024>(p, stream)
+         : nt == 512 ? launch_cluster<CL, 512>(p, stream)
+                     : launch_cluster<CL, 256>(p, stream);
+}
+
+// A cluster's CTAs lie in one GPC, so clusters that hold one CTA per SM leave
+// some SMs out: of this GPU's 152, 152, 76, 36, 15 and 7 clusters of 1 to 16 run
+// at once (cudaOccupancyMaxActiveClusters).  A CTA has 1024 threads where all
+// clusters run at once like that, 512 or 256 where two or four CTAs have to share
+// an SM.  Clusters are as large as leaves every SM a CTA at most and a CTA 2048
+// rows, and as few as hold the keys.
 cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.MBS * kPageSize, segs = (int64_t)p.B * p.Hkv;
+  auto at_once = [&](int cl) -> int64_t {
+    return cl == 1 ? sms : cl == 2 ? sms / 2 : cl == 4 ? sms * 36 / 152 : cl == 8 ? sms / 10 : sms / 21;
+  };
   int cl = 1;
   while (cl < kMaxCluster && (smem_of(rows, cl) > kSmemLimit ||
-                              (segs * 2 * cl <= sms && rows / (2 * cl) >= 2048)))
+                              (segs <= at_once(2 * cl) && rows >= (int64_t)2 * cl * 2048)))
     cl *= 2;
+  const int nt = segs <= at_once(cl) ? 1024 : segs <= 2 * at_once(cl) ? 512 : 256;
   switch (cl) {
-    case 1: return launch_cluster<1>(p, stream);
-    case 2: return launch_cluster<2>(p, stream);
-    case 4: return launch_cluster<4>(p, stream);
-    default: return launch_cluster<8>(p, stream);
+    case 1: return launch_threads<1>(p, nt, stream);
+    case 2: return launch_threads<2>(p, nt, stream);
+    case 4: return launch_threads<4>(p, nt, stream);
+    case 8: return launch_threads<8>(p, nt, stream);
+    default: return launch_threads<16>(p, nt, stream);
   }
 }
 

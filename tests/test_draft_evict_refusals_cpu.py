@@ -95,7 +95,7 @@ def evict(x=None, kc=F, vc=F, w=F, pos=F, tab=F, ctx=F, old=F, told=F, B=2, mbs=
     (dict(new=ODD), INV), (dict(budget=0), INV), (dict(budget=-1), INV), (dict(sinks=-1), INV),
     (dict(recent=-1), INV), (dict(sinks=6, recent=3), INV),
     (dict(budget=2 ** 31 - 1, sinks=2 ** 31 - 1, recent=2 ** 31 - 1), INV),
-    (dict(B=-1), INV), (dict(mbs=0), INV), (dict(mbs=24577), UNS), (dict(x=desc(d=96)), UNS),
+    (dict(B=-1), INV), (dict(mbs=0), INV), (dict(mbs=49153), UNS), (dict(x=desc(d=96)), UNS),
     (dict(new=F), INV), (dict(new=ctypes.c_void_p(0x10000 - 4)), INV),
     (dict(B=0, kc=None), pkv.PKV_OK),
 ])
