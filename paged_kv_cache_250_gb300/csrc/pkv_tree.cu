@@ -15,7 +15,7 @@
 // cut leaves a partial in each CTA: slot 2 c where it came from the CTA before,
 // 2 c + 1 where it starts in c.  Roles hand over through mbarriers:
 //   warps 0-3, 4-7  softmax of stream 0, 1: one row per thread, TMEM lane t;
-//   warp 8          issues the MMAs; warp 9 the tensor copies.
+//   warp 8          issues the MMAs; warp 9 the copies of Q and K, warp 10 those of V.
 // A stream is a row tile with its accumulator.  Two tiles share every block (K
 // and V double-buffered).  Where a pair has one tile (up to 128 rows: the usual
 // tree), both streams are that tile, stream t taking every second block in
@@ -39,7 +39,7 @@ namespace tr {
 
 constexpr int kRows = kTreeRows, kTok = kTreeTok;
 constexpr int kPages = kTok / kPageSize;
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr uint32_t kHalf = 16384;  // 128 rows x 128 bytes: 64 d columns of a tile or block
 // one barrier per buffer or stream, in pairs
 constexpr int kBarQ = 0, kBarQFree = 2, kBarKFull = 4, kBarVFull = 6, kBarKFree = 8,
@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
-  if (warp == 9) {
+  if (warp >= 9) {
+    const bool v = warp == 10;  // V, else Q and K: neither waits for the other's buffers
     // ------------------------------------------------------------ copies
     bool ok = true;
     while (ok && next()) {
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return lane < kPages && t < streams && i < wk.count(t) && pg < pages ? table[pg] : 0;
       };
       int cur0 = entry(0, 0), cur1 = entry(1, 0);
-      for (int t = 0; ok && t < (wk.s.two ? 2 : 1); ++t) {
+      for (int t = 0; ok && !v && t < (wk.s.two ? 2 : 1); ++t) {
         const int sl = wk.slot(t), u = wk.slot_use(sl);
         if (u > 0) ok = __all_sync(0xffffffffu, wait(kBarQFree + sl, (uint32_t)((u - 1) & 1)));
         if (!ok) break;
@@ -228,34 +229,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int i = 0; ok && i < wk.count(0); ++i) {
         const int nxt0 = entry(0, i + 1), nxt1 = entry(1, i + 1);
-        for (int v = 0; ok && v < 2; ++v) {  // K of the streams, then V
-          for (int t = 0; t < streams; ++t) {
-            if (i >= wk.count(t)) continue;
-            const int bb = wk.buf(t, i), u = wk.use(t, i);
-            const int npg = min(kPages, pages - wk.block(t, i) * kPages);
-            int blk = t == 0 ? cur0 : cur1;
-            if (lane < npg && (blk < 0 || blk >= p.NB)) {  // zeros, past the pool
-              if (v == 0) report_error(p.err_word, PKV_ERR_BOUNDS);
-              blk = p.NB;
-            }
-            const int full = (v ? kBarVFull : kBarKFull) + bb;
-            if (u > 0)
-              ok = __all_sync(0xffffffffu,
-                              wait((v ? kBarVFree : kBarKFree) + bb, (uint32_t)((u - 1) & 1)));
-            if (!ok) break;
-            if (lane == 0) {
-              armed[full] = armed[full] + 1;
-              mbar_arrive_expect_tx(bar(full), (uint32_t)npg * NH * kPageSize * 128);
-            }
-            __syncwarp();
-            if (lane < npg) {
-              const uint32_t dst = base + (v ? kOffV : kOffK) + (uint32_t)bb * NH * kHalf +
-                                   (uint32_t)lane * kPageSize * 128;
-              const int r = (blk * p.Hkv + wk.s.h) * kPageSize;
-              for (int c = 0; c < NH; ++c)
-                tma_load_2d_plain(dst + (uint32_t)c * kHalf,
-                                  v ? (const void*)&tmv : (const void*)&tmk, bar(full), c * 64, r);
-            }
+        for (int t = 0; t < streams; ++t) {
+          if (i >= wk.count(t)) continue;
+          const int bb = wk.buf(t, i), u = wk.use(t, i);
+          const int npg = min(kPages, pages - wk.block(t, i) * kPages);
+          int blk = t == 0 ? cur0 : cur1;
+          if (lane < npg && (blk < 0 || blk >= p.NB)) {  // zeros, past the pool
+            if (!v) report_error(p.err_word, PKV_ERR_BOUNDS);
+            blk = p.NB;
+          }
+          const int full = (v ? kBarVFull : kBarKFull) + bb;
+          if (u > 0)
+            ok = __all_sync(0xffffffffu,
+                            wait((v ? kBarVFree : kBarKFree) + bb, (uint32_t)((u - 1) & 1)));
+          if (!ok) break;
+          if (lane == 0) {
+            armed[full] = armed[full] + 1;
+            mbar_arrive_expect_tx(bar(full), (uint32_t)npg * NH * kPageSize * 128);
+          }
+          __syncwarp();
+          if (lane < npg) {
+            const uint32_t dst = base + (v ? kOffV : kOffK) + (uint32_t)bb * NH * kHalf +
+                                 (uint32_t)lane * kPageSize * 128;
+            const int r = (blk * p.Hkv + wk.s.h) * kPageSize;
+            for (int c = 0; c < NH; ++c)
+              tma_load_2d_plain(dst + (uint32_t)c * kHalf,
+                                v ? (const void*)&tmv : (const void*)&tmk, bar(full), c * 64, r);
           }
         }
         ok = ok && !__any_sync(0xffffffffu, *abort_flag != 0);
