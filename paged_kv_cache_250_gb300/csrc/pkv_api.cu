@@ -259,14 +259,15 @@ ScoredLayout scored_layout(const pkv_cache_desc* d, int32_t batch, int32_t mbs) 
   return s;
 }
 
-// Tree attention: two partial slots of 256 rows per CTA, whatever the batch.
+// Tree attention: two partial slots of 256 rows per CTA for line 2 of the work and
+// two of 128 for each of its two shares of line 1, whatever the batch.
 struct TreeLayout {
   size_t ml, o, total;
 };
 TreeLayout tree_layout(const pkv_cache_desc* d, int sms) {
-  const size_t rows = (size_t)sms * 2 * 2 * pkv::kTreeRows;
+  const size_t rows = (size_t)sms * 8 * pkv::kTreeRows;
   TreeLayout t;
-  t.ml = align256((size_t)sms * sizeof(int4));
+  t.ml = align256((size_t)sms * 3 * 2 * sizeof(int4));
   t.o = align256(t.ml + rows * sizeof(float2));
   t.total = align256(t.o + rows * d->head_dim * sizeof(float));
   return t;
@@ -828,12 +829,14 @@ pkv_status pkv_paged_tree_attention(
   l.p.MBS = max_blocks_per_seq;
   l.p.total_q = total_q;
   l.p.max_q = max_q_len;
-  // as many CTAs as the longest sequences the arguments allow would keep busy
+  // as many CTAs as the longest sequences the arguments allow would keep busy; the
+  // kernel's costs are 32-bit sums
   const int rows = max_q_len * (desc->num_q_heads / desc->num_kv_heads);
-  l.p.ctas = (int32_t)pkv::tree_shares(
-      batch * pkv::tree_seq_cost(desc->num_kv_heads, rows,
-                                 pkv::tree_blocks(max_blocks_per_seq * kPageSize)),
-      sms);
+  const int nblk = pkv::tree_blocks(max_blocks_per_seq * kPageSize);
+  const int64_t segs = (int64_t)batch * desc->num_kv_heads * ((rows + 127) / 128);
+  if (segs >= ((int64_t)1 << 31) || segs * pkv::tree_seg_cost(nblk) >= ((int64_t)1 << 32))
+    return PKV_ERR_UNSUPPORTED;
+  l.p.ctas = (int32_t)pkv::tree_shares(segs * pkv::tree_seg_cost(nblk), sms < 256 ? sms : 256);
   l.p.out_dtype = out_dtype;
   l.p.scale_log2 = scale * 1.4426950408889634f;
   l.bf16 = desc->cache_dtype == PKV_BF16;

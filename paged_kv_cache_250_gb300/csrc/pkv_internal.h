@@ -411,11 +411,12 @@ struct TreeParams {
   const int32_t* q_start;        // [B+1]
   const int64_t* tree_mask;      // [total_q]
   void* out;                     // [total_q][Hq][d]
-  // Partials: CTA c's part of a segment that began before it in slot 2 c, of one
-  // that begins in it and goes on in 2 c + 1: [slot][256 rows].
+  // Partials: share c's part of a segment that began before it in slot 2 c, of one
+  // that begins in it and goes on in 2 c + 1: the slots of line 2, 256 rows each,
+  // for `ctas` shares, then those of line 1, 128 rows each, for 2 ctas.
   float2* part_ml;               // (m in log2 units, l)
   float* part_o;                 // [d] each, unnormalised
-  int4* meta;                    // [ctas] what each CTA left, for the merge
+  int4* meta;                    // [3 ctas][2] what each share left, for the merge
   int32_t* err_word;
   int32_t B, Hq, Hkv, NB, MBS, total_q, max_q;
   int32_t ctas;

@@ -1,12 +1,13 @@
 // pkv_tree_line.h -- how the tree kernel's work is cut into shares.  Needs no CUDA.
 //
-// A segment is (sequence, pair of 128-row tiles, KV head): the rows are the
-// sequence's nodes times the g query heads of the KV head, 256 to a pair.  Its
-// units are the blocks of 128 cached tokens.  The segments lie on one line,
-// sequence by sequence, pair by pair, head by head, where a segment's start
-// costs kTreeSeg and a block kTreeTwo, or kTreeOne where the pair's second tile
-// is empty.  The line is cut into n equal shares, one per CTA; a unit belongs to
-// the share that its first cost lies in.
+// The rows of a (sequence, KV head), its nodes times the g query heads of the KV
+// head, are cut into pairs of 128-row tiles, and what is left beyond whole pairs
+// into one more: a pair whose second tile holds rows is a segment of line 2, the
+// last one without a segment of line 1.  A segment's units are the blocks of 128
+// cached tokens.  Each line holds its segments sequence by sequence, head by
+// head, pair by pair, where a segment's start costs kTreeSeg and a block
+// kTreeBlock, and is cut into equal shares; a unit belongs to the share that its
+// first cost lies in.
 #pragma once
 
 #include "pkv_hd.h"
@@ -14,62 +15,60 @@
 namespace pkv {
 
 constexpr int kTreeRows = 128, kTreeTok = 128;  // rows of a tile, tokens of a block
-constexpr int kTreeOne = 3, kTreeTwo = 5, kTreeSeg = 4;
-constexpr int kTreeMinShare = 8;  // a share is worth at least this much
-constexpr int kTreeMaxBatch = 4000;
+constexpr int kTreeBlock = 2, kTreeSeg = 3;
+constexpr int kTreeMinShare = 4;  // a share is worth at least this much
+constexpr int kTreeMaxBatch = 3840;
+static_assert(kTreeMinShare >= kTreeBlock, "no share without a block inside a segment");
 
 PKV_HD int tree_blocks(int ctx) { return (int)(((int64_t)ctx + kTreeTok - 1) / kTreeTok); }
-PKV_HD int tree_pairs(int rows) { return (rows + 2 * kTreeRows - 1) / (2 * kTreeRows); }
-PKV_HD bool tree_two(int rows, int pair) { return rows > (2 * pair + 1) * kTreeRows; }
-PKV_HD int64_t tree_seg_cost(int rows, int pair, int nblk) {
-  return kTreeSeg + (int64_t)nblk * (tree_two(rows, pair) ? kTreeTwo : kTreeOne);
+// segments of a (sequence, KV head) on line 2 (two) or 1, and the first row of one
+PKV_HD int tree_segs(bool two, int rows) {
+  const int pairs = (rows + kTreeRows - 1) / (2 * kTreeRows);  // with two tiles
+  return two ? pairs : rows > 2 * kTreeRows * pairs ? 1 : 0;
 }
-// whole cost of a sequence (0 where it has no rows)
-PKV_HD int64_t tree_seq_cost(int Hkv, int rows, int nblk) {
-  const int pairs = tree_pairs(rows);
-  if (pairs == 0) return 0;
-  return Hkv * ((pairs - 1) * tree_seg_cost(2 * kTreeRows, 0, nblk) +
-                tree_seg_cost(rows, pairs - 1, nblk));
+PKV_HD int tree_row0(bool two, int rows, int seg) {
+  return 2 * kTreeRows * (two ? seg : tree_segs(true, rows));
 }
-// CTAs that get work, of `launched`
-PKV_HD int64_t tree_shares(int64_t cost, int64_t launched) {
+// (Costs along a line are 32-bit: a call whose line could be longer is refused.)
+PKV_HD uint32_t tree_seg_cost(int nblk) { return kTreeSeg + (uint32_t)nblk * kTreeBlock; }
+// whole cost of a sequence on a line
+PKV_HD int64_t tree_seq_cost(bool two, int Hkv, int rows, int nblk) {
+  return (int64_t)Hkv * tree_segs(two, rows) * tree_seg_cost(nblk);
+}
+// Shares that get work, of at most `most`.
+PKV_HD int64_t tree_shares(int64_t cost, int64_t most) {
   const int64_t n = cost / kTreeMinShare;
-  return n < 1 ? 1 : n < launched ? n : launched;
+  return n < 1 ? 1 : n < most ? n : most;
 }
 PKV_HD int64_t tree_share(int64_t c, int64_t cost, int64_t n) {  // first cost of share c
   return udiv64(c * cost + n - 1, n);
 }
+PKV_HD int64_t tree_share_of(int64_t x, int64_t cost, int64_t n) {  // the share that x lies in
+  return udiv64(x * n, cost);
+}
 
-// One CTA's blocks j0 .. j0 + nblk - 1 of the `total` of a segment.
+// A share's blocks j0 .. j0 + nblk - 1 of the `total` of a segment.
 struct TreePart {
-  int b, pair, h, j0, nblk, total;
-  bool two;
+  int b, h, row0, j0, nblk, total;
 };
-// The segment at offset r of a sequence's stretch of the line, cut by `left`, the
+// The segment at offset r of a sequence's stretch of a line, cut by `left`, the
 // costs from there to the share's end.  Returns the costs from r to the segment's
 // end; s.nblk may be 0.
-PKV_HD int64_t tree_part(int Hkv, int rows, int nblk, int64_t r, int64_t left, TreePart& s) {
-  const int pairs = tree_pairs(rows);
-  const int64_t whole = Hkv * tree_seg_cost(2 * kTreeRows, 0, nblk);
-  s.pair = 0;
-  if (pairs > 1) {
-    const int64_t at = udiv64(r, whole);
-    s.pair = at < pairs - 1 ? (int)at : pairs - 1;
-  }
-  s.two = tree_two(rows, s.pair);
-  const int w = s.two ? kTreeTwo : kTreeOne;
-  const int64_t seg = tree_seg_cost(rows, s.pair, nblk);
-  r -= s.pair * whole;
-  s.h = (int)udiv64(r, seg);
-  r -= s.h * seg;
-  // block j begins at kTreeSeg + j w
-  auto first = [&](int64_t x) -> int64_t {
-    return x <= kTreeSeg ? 0 : udiv64(x - kTreeSeg + w - 1, w);
+PKV_HD uint32_t tree_part(bool two, int rows, int nblk, uint32_t r, uint32_t left, TreePart& s) {
+  const uint32_t seg = tree_seg_cost(nblk);
+  const int per = tree_segs(two, rows);
+  const int at = (int)(r / seg);
+  r -= (uint32_t)at * seg;
+  s.h = per == 1 ? at : at / per;
+  s.row0 = tree_row0(two, rows, at - s.h * per);
+  // block j begins at kTreeSeg + j kTreeBlock
+  auto first = [&](uint32_t x) -> int {
+    if (x >= seg) return nblk;
+    return x <= kTreeSeg ? 0 : (int)((x - kTreeSeg + kTreeBlock - 1) / kTreeBlock);
   };
-  const int64_t j0 = first(r), j1 = first(r + left);
   s.total = nblk;
-  s.j0 = (int)(j0 < nblk ? j0 : nblk);
-  s.nblk = (int)(j1 < nblk ? j1 : nblk) - s.j0;
+  s.j0 = first(r);
+  s.nblk = first(left < seg - r ? r + left : seg) - s.j0;
   return seg - r;
 }
 

@@ -24,82 +24,94 @@ static int fail(const char* what, long a, long b) {
   return 1;
 }
 
-static int walk(const std::vector<int>& rows, const std::vector<int>& ctx, int Hkv, int launched) {
+// One line of the work (two: segments of two tiles).
+static int walk(bool two, const std::vector<int>& rows, const std::vector<int>& ctx, int Hkv,
+                int most) {
   const int B = (int)rows.size();
-  std::vector<int64_t> pfx(B + 1, 0);
+  std::vector<int64_t> line(B + 1, 0);
   for (int b = 0; b < B; ++b)
-    pfx[b + 1] = pfx[b] + tree_seq_cost(Hkv, rows[b], tree_blocks(ctx[b]));
-  const int64_t cost = pfx[B], n = tree_shares(cost, launched);
-  if (n < 1 || n > launched) return fail("shares", n, launched);
-  std::map<std::tuple<int, int, int>, std::vector<int>> seen;   // segment -> blocks, in order
-  struct Meta { bool tail = false, head = false, head_ends = false; std::tuple<int, int, int> seg, head_seg; };
-  std::vector<Meta> meta(launched);
+    line[b + 1] = line[b] + tree_seq_cost(two, Hkv, rows[b], tree_blocks(ctx[b]));
+  const int64_t cost = line[B], n = tree_shares(cost, most);
+  if (n < 1 || n > most) return fail("shares", n, most);
+  std::map<std::tuple<int, int, int>, std::vector<int>> seen;   // segment -> shares of its blocks
+  struct Left { int parts = 0; std::tuple<int, int, int> seg; };  // where a segment starts
+  std::vector<Left> left(most);
+  std::vector<std::tuple<int, int, int>> head(most, {-1, -1, -1});
   int64_t longest = 0;
   for (int64_t c = 0; c < n; ++c) {
-    int64_t at = tree_share(c, cost, n);
-    const int64_t hi = tree_share(c + 1, cost, n);
+    int64_t at = cost ? tree_share(c, cost, n) : 0;
+    const int64_t hi = cost ? tree_share(c + 1, cost, n) : 0;
     if (c == 0 && at != 0) return fail("start", at, 0);
     if (c == n - 1 && hi != cost) return fail("end", hi, cost);
-    int parts = 0;
+    longest = std::max(longest, hi - at);
+    int parts = 0, b = 0;
     while (at < hi) {
-      int a = 0, z = B;
-      while (z - a > 1) {
-        const int mid = (a + z) >> 1;
-        if (pfx[mid] <= at) a = mid; else z = mid;
-      }
-      if (rows[a] == 0) return fail("empty sequence", a, at);
+      while (line[b + 1] <= at) ++b;
       TreePart s;
-      s.b = a;
-      const int64_t step = tree_part(Hkv, rows[a], tree_blocks(ctx[a]), at - pfx[a], hi - at, s);
+      s.b = b;
+      const int64_t step = tree_part(two, rows[b], tree_blocks(ctx[b]), at - line[b], hi - at, s);
       if (step <= 0) return fail("step", step, at);
       at += step;
       if (s.nblk <= 0) continue;
-      if (s.pair >= tree_pairs(rows[a]) || s.h >= Hkv || s.pair < 0 || s.h < 0)
-        return fail("segment", s.pair, s.h);
-      if (s.two != tree_two(rows[a], s.pair)) return fail("two", a, s.pair);
-      const auto key = std::make_tuple(a, s.pair, s.h);
+      if (s.h < 0 || s.h >= Hkv || s.row0 < 0 || s.row0 >= rows[b] || s.row0 % 256)
+        return fail("segment", s.row0, s.h);
+      if ((rows[b] - s.row0 > 128) != two) return fail("tiles", rows[b], s.row0);
+      const auto key = std::make_tuple(b, s.row0, s.h);
       auto& v = seen[key];
       for (int j = 0; j < s.nblk; ++j) {
         if ((int)v.size() != s.j0 + j) return fail("order", v.size(), s.j0 + j);
         v.push_back((int)c);
       }
-      const bool head = s.j0 > 0, ends = s.j0 + s.nblk == s.total;
-      if (head) {
-        if (parts != 0) return fail("head is not the first part", c, parts);
-        meta[c].head = true;
-        meta[c].head_ends = ends;
-        meta[c].head_seg = key;
+      const bool ends = s.j0 + s.nblk == s.total;
+      if (s.j0 > 0) {
+        if (parts != 0) return fail("not the first part", c, parts);
+        head[c] = key;
       } else if (!ends) {
-        if (meta[c].tail) return fail("two tails", c, parts);
-        meta[c].tail = true;
-        meta[c].seg = key;
+        if (left[c].parts) return fail("two that go on", c, parts);
+        left[c].parts = (int)(tree_share_of(at - kTreeBlock, cost, n) - c) + 1;
+        left[c].seg = key;
       }
       ++parts;
     }
-    longest = std::max(longest, hi - tree_share(c, cost, n));
   }
   if (longest > (cost + n - 1) / n) return fail("longest", longest, cost / n);
-  for (int b = 0; b < B; ++b)
-    for (int pr = 0; pr < tree_pairs(rows[b]); ++pr)
-      for (int h = 0; h < Hkv; ++h) {
-        auto it = seen.find(std::make_tuple(b, pr, h));
-        if (it == seen.end() || (int)it->second.size() != tree_blocks(ctx[b]))
-          return fail("blocks", b, pr);
-      }
+  size_t segs = 0;
+  for (int b = 0; b < B; ++b) segs += (size_t)Hkv * tree_segs(two, rows[b]);
+  if (seen.size() != segs) return fail("segments", seen.size(), segs);
   int cut = 0;
-  for (auto& kv : seen) cut += kv.second.front() != kv.second.back();
-  for (int c = 0; c < launched; ++c) {
-    if (!meta[c].tail) continue;
+  for (auto& kv : seen) {
+    if ((int)kv.second.size() != tree_blocks(ctx[std::get<0>(kv.first)]))
+      return fail("blocks", std::get<0>(kv.first), std::get<1>(kv.first));
+    cut += kv.second.front() != kv.second.back();
+  }
+  for (int c = 0; c < most; ++c) {
+    if (!left[c].parts) continue;
     --cut;
-    int last = c + 1;
-    while (last < launched - 1 && !meta[last].head_ends) ++last;
-    for (int k = c + 1; k <= last; ++k)
-      if (k >= launched || !meta[k].head || meta[k].head_seg != meta[c].seg)
-        return fail("part", c, k);
-    if (!meta[last].head_ends || seen[meta[c].seg].back() != last) return fail("last", c, last);
+    for (int k = c + 1; k < c + left[c].parts; ++k)
+      if (k >= most || head[k] != left[c].seg) return fail("part", c, k);
+    if (left[c].parts < 2 || seen[left[c].seg].back() != c + left[c].parts - 1)
+      return fail("last", c, left[c].parts);
   }
   if (cut != 0) return fail("cut segments", cut, 0);
   return 0;
+}
+
+// Both lines, for `ctas` CTAs; every row in one segment.
+static int both(const std::vector<int>& rows, const std::vector<int>& ctx, int Hkv, int ctas) {
+  for (size_t b = 0; b < rows.size(); ++b) {
+    int next = 0;
+    for (int s = 0; s < tree_segs(true, rows[b]); ++s) {
+      if (tree_row0(true, rows[b], s) != next) return fail("rows of line 2", b, s);
+      next += 256;
+    }
+    if (tree_segs(false, rows[b])) {
+      if (tree_row0(false, rows[b], 0) != next) return fail("rows of line 1", b, next);
+      next += 128;
+    }
+    if (next < rows[b] || (rows[b] == 0 && next)) return fail("rows", rows[b], next);
+  }
+  const int r = walk(true, rows, ctx, Hkv, ctas);
+  return r ? r : walk(false, rows, ctx, Hkv, 2 * ctas);
 }
 
 int main() {
@@ -115,15 +127,15 @@ int main() {
       rows.push_back(n * G);
       ctx.push_back(n + draw(0, most));
     }
-    if (int r = walk(rows, ctx, Hkv, launched)) { std::printf("iteration %d\n", it); return r; }
+    if (int r = both(rows, ctx, Hkv, launched)) { std::printf("iteration %d\n", it); return r; }
   }
-  if (walk({0, 0}, {5, 0}, 2, 152)) return 1;
-  if (walk({512}, {2147483647}, 8, 152)) return 1;
-  std::vector<int> many(4000, 512), far(4000, 8000000);
-  if (walk({512, 8, 0, 136}, {64, 1, 0, 2147483000}, 1, 152)) return 1;
-  int64_t c = 0;
-  for (int b = 0; b < 4000; ++b) c += tree_seq_cost(8, many[b], tree_blocks(far[b]));
-  if (tree_share(152, c, 152) != c || tree_shares(c, 152) != 152) return 1;
+  if (both({0, 0}, {5, 0}, 2, 152)) return 1;
+  if (both({512}, {2147483647}, 1, 152)) return 1;
+  if (both({512, 8, 0, 136}, {64, 1, 0, 2147483000}, 1, 152)) return 1;
+  const int64_t far = ((int64_t)1 << 32) - 1;  // the largest cost a call may have
+  if (tree_share(152, far, 152) != far || tree_shares(far, 152) != 152 ||
+      tree_share_of(far - 1, far, 304) != 303)
+    return 1;
   std::puts("ok");
   return 0;
 }
