@@ -836,7 +836,8 @@ pkv_status pkv_paged_tree_attention(
   const int64_t segs = (int64_t)batch * desc->num_kv_heads * ((rows + 127) / 128);
   if (segs >= ((int64_t)1 << 31) || segs * pkv::tree_seg_cost(nblk) >= ((int64_t)1 << 32))
     return PKV_ERR_UNSUPPORTED;
-  l.p.ctas = (int32_t)pkv::tree_shares(segs * pkv::tree_seg_cost(nblk), sms < 256 ? sms : 256);
+  l.p.ctas = (int32_t)pkv::tree_shares(segs * pkv::tree_seg_cost(nblk),
+                                       sms < pkv::kTreeMaxCtas ? sms : pkv::kTreeMaxCtas);
   l.p.out_dtype = out_dtype;
   l.p.scale_log2 = scale * 1.4426950408889634f;
   l.bf16 = desc->cache_dtype == PKV_BF16;

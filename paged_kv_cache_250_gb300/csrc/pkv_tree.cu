@@ -57,7 +57,8 @@ struct Plan {
   static constexpr uint32_t kOffBar = 6 * NH * kHalf;
   static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;     // TMEM base, abort, counts
   static constexpr uint32_t kOffSeq = (kOffMisc + 24 + 4 * kNumBars + 15) / 16 * 16;  // [kSeqs]
-  static constexpr uint32_t kOffPfx = kOffSeq + 16 * kSeqs;  // [2][B+1]
+  static constexpr uint32_t kOffBounds = kOffSeq + 16 * kSeqs;  // [3]
+  static constexpr uint32_t kOffPfx = kOffBounds + 48;          // [2][B+1]
   static constexpr size_t smem(int B) { return 1024 + kOffPfx + 8 * ((size_t)B + 1); }
 };
 static_assert(Plan<128>::smem(kTreeMaxBatch) <= 227 * 1024, "the largest batch fits");
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* bad_pages = reinterpret_cast<volatile uint32_t*>(
       base_ptr + PL::kOffMisc + 8 + 4 * kNumBars);  // of K's buffers, two uses each
   int4* seqs = reinterpret_cast<int4*>(base_ptr + PL::kOffSeq);  // (q0, n, ctx)
+  uint4* bounds = reinterpret_cast<uint4*>(base_ptr + PL::kOffBounds);
   uint32_t* pfx = reinterpret_cast<uint32_t*>(base_ptr + PL::kOffPfx);  // [2][B+1] costs before
 
   if (tid == 0) {
@@ -159,21 +161,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   } wk;
   const uint32_t* line = pfx;
   bool two = false;
-  auto begin = [&](bool t2, int share, int most) {  // of `most` shares at most
-    two = t2;
-    line = pfx + (t2 ? p.B + 1 : 0);
-    const int64_t cost = line[p.B], n = tree_shares(cost, most);
-    wk.share = share;
-    wk.at = share < n ? (uint32_t)tree_share(share, cost, n) : 0;
-    wk.hi = share < n ? (uint32_t)tree_share(share + 1, cost, n) : 0;
-    int a = 0;  // the sequence holding `at`: the last with line <= at
-    if (wk.at < wk.hi) {
+  // k: the CTA's share of line 2 (0), its streams' of line 1 (1, 2), whose first
+  // shares go to CTAs of their own.  Their bounds are looked up once, by a thread each.
+  const int grid = gridDim.x;
+  if (tid < 3) {
+    const uint32_t* ln = pfx + (tid == 0 ? p.B + 1 : 0);
+    const int share = tid < 2 ? blockIdx.x : grid + blockIdx.x;
+    const int64_t cost = ln[p.B], n = tree_shares(cost, tid == 0 ? grid : 2 * grid);
+    uint32_t from = 0, to = 0;
+    int a = 0;  // the sequence holding `from`: the last with ln <= from
+    if (share < n && cost > 0) {
+      from = (uint32_t)tree_share(share, cost, n);
+      to = (uint32_t)tree_share(share + 1, cost, n);
       for (int z = p.B; z - a > 1;) {
         const int mid = (a + z) >> 1;
-        if (line[mid] <= wk.at) a = mid; else z = mid;
+        if (ln[mid] <= from) a = mid; else z = mid;
       }
     }
-    wk.s.b = a;
+    bounds[tid] = make_uint4(from, to, (uint32_t)a, (uint32_t)share);
+  }
+  __syncthreads();
+  auto begin = [&](int k) {
+    const uint4 v = bounds[k];
+    two = k == 0;
+    line = pfx + (two ? p.B + 1 : 0);
+    wk.at = v.x;
+    wk.hi = v.y;
+    wk.s.b = (int)v.z;
+    wk.share = (int)v.w;
   };
   auto next = [&]() -> bool {
     while (wk.at < wk.hi) {
@@ -192,11 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return false;
   };
-  const int grid = gridDim.x;
-  auto begin2 = [&]() { begin(true, blockIdx.x, grid); };
-  // the first shares of line 1 go to CTAs of their own
-  auto begin1 = [&](int t) { begin(false, t * grid + blockIdx.x, 2 * grid); };
-
   auto wait = [&](int i, uint32_t parity) -> bool {
     if (mbar_try_wait(bar(i), parity)) return true;
     if (*abort_flag) return false;
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  ? p.block_tables[(int64_t)wk.s.b * p.MBS + pg] : 0;
     };
     const bool v = warp == 10;
-    begin2();  // warp 9: Q and K, warp 10: V
+    begin(0);  // warp 9: Q and K, warp 10: V
     while (ok && next()) {
       int cur = entry(wk.s.j0);
       for (int t = 0; ok && t < 2; ++t) {
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     const int t = warp - 9;
-    begin1(t);  // each a stream
+    begin(1 + t);  // each a stream
     while (ok && next()) {
       int cur = entry(wk.s.j0);
       load_q(t, wk.s.row0);
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The first product over O_t of a part comes after P_t, which the softmax
       // threads hand over after they have read the last part's O_t out.
       if (elect_one()) {
-        begin2();
+        begin(0);
         while (ok && next()) {  // one buffer after the other, both streams from it
           const int n = wk.s.nblk;
           if (warp == 8) {  // (warp 11 counts)
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kBarODone + 1, (st - 1) & 1);
           tc_fence_after();
         }
-        begin1(t);
+        begin(1 + t);
         while (ok && next()) {
           ok = wait(kBarQ + t, segs++ & 1);
           for (int i = 0; ok && i < wk.s.nblk; ++i, ++u, ++st) {
@@ -396,8 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2;           // stream
     const int tt = tid - t * kRows;    // row in the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + (uint32_t)t * kTok + lane_base;
+    const uint32_t t_sc = tmem + (uint32_t)t * kTok + lane_base;
     const uint32_t t_o = tmem + 256 + (uint32_t)t * D + lane_base;
+    // 128 columns that hold nothing before the stream's first P is handed over
+    const uint32_t t_free = D == 64 ? tmem + 384 + lane_base : t_o;
+    bool cold = true;
     const float c2 = p.scale_log2;
     bool ok = true;
     int done = 0;            // blocks of the stream so far
@@ -406,8 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the first (as two words)
     int4 left = make_int4(0, 0, 0, 0), left_at = left;
     for (int ln = 0; ln < 2; ++ln) {  // line 2, then the stream's share of line 1
-    if (ln == 0) begin2();
-    else begin1(t);
+    begin(ln == 0 ? 0 : 1 + t);
     while (ok && next()) {
       const int nt = wk.s.nblk;
       int tok0 = wk.s.j0 * kTok;
@@ -423,18 +435,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
              __reduce_or_sync(0xffffffffu, (uint32_t)any)) & nodes;
       float m_ref = -INFINITY, l_sum = 0.f;
-      for (int i = 0; ok && i < nt; ++i, tok0 += kTok) {
+      // The first part begins with a step on whatever lies in columns that no product
+      // uses yet, and drops what comes out: it brings the instructions into the cache
+      // while the first blocks are on their way (about 5000 cycles else).
+      int i = cold ? -1 : 0;
+      cold = false;
+      if (i < 0) tok0 -= kTok;
+      for (; ok && i < nt; ++i, tok0 += kTok) {
         const int kb = two ? i & 1 : t;  // the block's buffers, and their uses before
         const int ku = (kb ? u1 : u0) + (two ? i >> 1 : i);
-        ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
-        if (!ok) break;
-        tc_fence_after();
+        const uint32_t t_s = i < 0 ? t_free : t_sc;
+        if (i >= 0) {
+          ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
+          if (!ok) break;
+          tc_fence_after();
+        }
         // a page outside the pool (reported by the copy warp, zeros in shared memory)
         // is left out: bit pg stands for the block's page pg
-        const uint32_t bad = bad_pages[2 * kb + (ku & 1)];
+        const uint32_t bad = i < 0 ? 0 : bad_pages[2 * kb + (ku & 1)];
         if (busy) {
         uint32_t sa[32], sb[32];
-        if (tok0 + kTok > past || bad != 0) {  // scores that the row does not see
+        if (i >= 0 && (tok0 + kTok > past || bad != 0)) {  // scores that the row does not see
 #pragma unroll 1
           for (int qq = 0; qq < 4; ++qq) {
             // bit e: whether the row sees token tok0 + 32 qq + e
@@ -457,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; ++e)
             m4[e & 3] = max3(m4[e & 3], __uint_as_float(sq[2 * e]), __uint_as_float(sq[2 * e + 1]));
         };
-        // quarters 3, 2, 1, 0: quarter 0 is still in sb when the P pass starts
+        // quarters 3, 2, 1, 0: quarter 0 is still in sb when the P pass starts.  (Loops
+        // over two quarters, not four: the code is fetched once per launch.)
         tmem_ld32_issue(t_s + 96, sa);
         tmem_ld_wait(sa);
         tmem_ld32_issue(t_s + 64, sb);
@@ -511,30 +533,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             lo16[e] = pack2<BF16>(l.x, l.y);
           }
         };
-        auto qst = [&](int qq) {
-          const uint32_t c = (uint32_t)(64 * (qq >> 1) + 16 * (qq & 1));
+        // P of the first 32 tokens of half c / 64, then of the others
+#pragma unroll
+        for (uint32_t c = 0; c < 128; c += 64) {
+          tmem_ld32_issue(t_s + c + 32, sa);
+          qp(sb);
+          tmem_ld_wait(sa);
           tmem_st16_issue(t_s + c, hi16);
           tmem_st16_issue(t_s + c + 32, lo16);
-        };
-        tmem_ld32_issue(t_s + 32, sa);
-        qp(sb);
-        tmem_ld_wait(sa);
-        qst(0);
-        tmem_ld32_issue(t_s + 64, sb);
-        qp(sa);
-        tmem_ld_wait(sb);
-        qst(1);
-        tmem_ld32_issue(t_s + 96, sa);
-        qp(sb);
-        tmem_ld_wait(sa);
-        qst(2);
-        qp(sa);
-        qst(3);
+          if (c == 0) tmem_ld32_issue(t_s + 64, sb);
+          qp(sa);
+          if (c == 0) tmem_ld_wait(sb);
+          tmem_st16_issue(t_s + c + 16, hi16);
+          tmem_st16_issue(t_s + c + 48, lo16);
+        }
         tmem_st_wait();
         {
           const float2 a0 = f2_split(add2(acc[0], acc[1])), a1 = f2_split(add2(acc[2], acc[3]));
           l_sum += (a0.x + a0.y) + (a1.x + a1.y);
         }
+        }
+        if (i < 0) {
+          m_ref = -INFINITY;
+          l_sum = 0.f;
+          continue;
         }
         // V rows behind the end, and of nodes that no row sees, may hold anything
         // (0 x NaN): zeroed in the staged block by the stream that uses it first
@@ -641,126 +663,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- the merge of the segments that share boundaries cut.  Every CTA lists them
-// (their groups of rows, summed up) and its warps take every grid-th group: a row
-// of a segment with many parts, eight parts in flight, or kMergeAt rows of one with
-// few.  (A grid over shares and rows, mostly empty, took 35 us, cold, for the
-// case of 32 ragged sequences.)
-constexpr int kMergeWarps = 8, kMergeAt = 4, kMergeFew = 4;
-constexpr int kMergeShares = 1024;  // room for the shares of both lines
-
-// kAt rows from r0 on of a segment by one warp, kFly parts in flight.
-template <int D, int kAt, int kFly, typename Slot>
-__device__ __forceinline__ void merge_rows(const TreeParams& p, Slot slot, int parts, int r0,
-                                           int rows, int64_t out0) {
-  constexpr int V = D / 32;  // columns per lane
-  const int lane = threadIdx.x & 31;
-  float M[kAt], acc[kAt][V], l[kAt];
-  bool in[kAt];
-#pragma unroll
-  for (int a = 0; a < kAt; ++a) {
-    in[a] = r0 + a < rows;
-    l[a] = 0.f;
-    M[a] = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[a][e] = 0.f;
-  }
-  auto ml_of = [&](int k, int a) -> float2 {
-    return in[a] && k < parts ? p.part_ml[slot(k) + r0 + a]
-                              : make_float2(-INFINITY, 0.f);
-  };
-  float2 ml[kAt];
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-#pragma unroll
-    for (int a = 0; a < kAt; ++a) {
-      ml[a] = ml_of(k0 + lane, a);
-      M[a] = fmaxf(M[a], ml[a].x);
-    }
-  }
-#pragma unroll
-  for (int a = 0; a < kAt; ++a) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M[a] = fmaxf(M[a], __shfl_xor_sync(0xffffffffu, M[a], o));
-    if (M[a] == -INFINITY) M[a] = 0.f;  // nothing at all, or nothing but NaN
-  }
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    if (parts > 32) {  // else they are at hand
-#pragma unroll
-      for (int a = 0; a < kAt; ++a) ml[a] = ml_of(k0 + lane, a);
-    }
-    for (int k1 = k0; k1 < k0 + 32 && k1 < parts; k1 += kFly) {
-      float x[kFly][kAt][V];
-#pragma unroll
-      for (int f = 0; f < kFly; ++f)
-#pragma unroll
-        for (int a = 0; a < kAt; ++a) {
-          const float lk = __shfl_sync(0xffffffffu, ml[a].y, k1 + f - k0);
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[f][a][e] = 0.f;
-          if (k1 + f >= parts || lk == 0.f) continue;  // a part with nothing in it
-          const float* from = p.part_o + (slot(k1 + f) + r0 + a) * D + lane * V;
-          if constexpr (V == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(from);
-            x[f][a][0] = v.x;
-            x[f][a][1] = v.y;
-            x[f][a][2] = v.z;
-            x[f][a][3] = v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(from);
-            x[f][a][0] = v.x;
-            x[f][a][1] = v.y;
-          }
-        }
-#pragma unroll
-      for (int f = 0; f < kFly; ++f)
-#pragma unroll
-        for (int a = 0; a < kAt; ++a) {
-          const float mk = __shfl_sync(0xffffffffu, ml[a].x, k1 + f - k0);
-          const float lk = __shfl_sync(0xffffffffu, ml[a].y, k1 + f - k0);
-          const float w = k1 + f < parts ? ex2(mk - M[a]) : 0.f;
-          l[a] += w * lk;
-#pragma unroll
-          for (int e = 0; e < V; ++e) acc[a][e] += w * x[f][a][e];
-        }
-    }
-  }
-#pragma unroll
-  for (int a = 0; a < kAt; ++a) {
-    if (!in[a]) continue;
-    const float inv = l[a] != 0.f ? 1.f / l[a] : 0.f;
-    const int G = p.Hq / p.Hkv, row = r0 + a;
-    const int64_t to = (out0 + (int64_t)(row / G) * p.Hq + row % G) * D + lane * V;
-    if (p.out_dtype == PKV_F32) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) static_cast<float*>(p.out)[to + e] = acc[a][e] * inv;
-    } else {
-      const bool bf = p.out_dtype == PKV_BF16;
-      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + to);
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e)
-        out[e] = bf ? pack2<true>(acc[a][2 * e] * inv, acc[a][2 * e + 1] * inv)
-                    : pack2<false>(acc[a][2 * e] * inv, acc[a][2 * e + 1] * inv);
-    }
-  }
-}
+// (their groups of rows, summed up) and its warps take every grid-th group.  Eight
+// lanes hold a row's columns: a warp joins four rows of a segment with few parts, or
+// the parts of one row of a segment with many, every fourth in eight lanes.  Bound
+// by latency: the launch, a round of loads, and the code, which is fetched anew by
+// every launch and therefore short (four rows per warp and lane unrolled took 22 us
+// for 35 MB of partials).
+constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeAt = 4, kMergeFew = 4;
+constexpr int kMergeShares = 768;  // room for the shares of both lines
+constexpr int kMaxCtas = kMergeShares / 3;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeParams p) {
-  __shared__ int upto[kMergeShares];      // groups up to and with a cut segment
-  __shared__ int16_t share[kMergeShares]; // its entry in meta
+__global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const TreeParams p) {
+  __shared__ int upto[kMergeShares];   // groups up to and with a cut segment
+  __shared__ int4 cut[kMergeShares];   // its entry of meta, parts and rows, first output row
   __shared__ int warp_n[kMergeWarps], warp_g[kMergeWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int cuts = 0, groups = 0;
-  for (int i0 = 0; i0 < 3 * p.ctas; i0 += kMergeWarps * 32) {
+  for (int i0 = 0; i0 < 3 * p.ctas; i0 += kMergeThreads) {
     const int i = i0 + tid;
-    const int4 m = i < 3 * p.ctas ? p.meta[2 * i] : make_int4(0, 0, 0, 0);
+    int4 m = make_int4(0, 0, 0, 0), o = m;
+    if (i < 3 * p.ctas) {
+      m = p.meta[2 * i];
+      o = p.meta[2 * i + 1];
+    }
     const int mine = m.x == 0 ? 0 : m.x > kMergeFew ? m.y : (m.y + kMergeAt - 1) / kMergeAt;
     int g = mine;  // groups up to this entry's
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, g, o);
-      if (lane >= o) g += v;
+    for (int o2 = 1; o2 < 32; o2 <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, g, o2);
+      if (lane >= o2) g += v;
     }
     const uint32_t any = __ballot_sync(0xffffffffu, mine > 0);
     if (lane == 31) {
@@ -768,42 +703,111 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
       warp_n[warp] = __popc(any);
     }
     __syncthreads();
-    int at = cuts + __popc(any & ((1u << lane) - 1));
-    g += groups;
-    for (int w = 0; w < kMergeWarps; ++w) {
-      if (w < warp) {
-        at += warp_n[w];
-        g += warp_g[w];
-      }
-      cuts += warp_n[w];
-      groups += warp_g[w];
-    }
+    const int wn = lane < kMergeWarps ? warp_n[lane] : 0, wg = lane < kMergeWarps ? warp_g[lane] : 0;
+    const int at = cuts + __reduce_add_sync(0xffffffffu, lane < warp ? wn : 0) +
+                   __popc(any & ((1u << lane) - 1));
+    g += groups + __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0);
+    cuts += __reduce_add_sync(0xffffffffu, wn);
+    groups += __reduce_add_sync(0xffffffffu, wg);
     if (mine > 0) {
       upto[at] = g;
-      share[at] = (int16_t)i;
+      cut[at] = make_int4(i | m.y << 16, m.x, o.x, o.y);
     }
     __syncthreads();
   }
-  for (int g = blockIdx.x * kMergeWarps + warp; g < groups; g += gridDim.x * kMergeWarps) {
+  constexpr int V = D / 32;  // groups of four columns of a lane
+  // group g of warp w of CTA c is w grid + c: a segment's rows spread over the SMs
+  for (int g = warp * gridDim.x + blockIdx.x; g < groups; g += gridDim.x * kMergeWarps) {
     int a = 0;  // the first cut segment whose sum is above g
     for (int z = cuts - 1; a < z;) {
       const int mid = (a + z) >> 1;
       if (upto[mid] > g) z = mid; else a = mid + 1;
     }
-    const int i = share[a], sub = g - (a > 0 ? upto[a - 1] : 0);
-    const int4 m = p.meta[2 * i], o = p.meta[2 * i + 1];
+    const int4 m = cut[a];
+    const int i = m.x & 0xffff, rows = m.x >> 16, parts = m.y;
+    const int sub = g - (a > 0 ? upto[a - 1] : 0);
     const bool two = i < p.ctas;
     const int c = two ? i : i - p.ctas, per = two ? 2 * kRows : kRows;
-    const int64_t out0 = (int64_t)(uint32_t)o.x | (int64_t)o.y << 32;
+    const int64_t out0 = (int64_t)(uint32_t)m.z | (int64_t)m.w << 32;
     // the parts: slot 2 c + 1, then 2 c' of the shares behind
     const int64_t first = two ? 0 : 4 * kRows * (int64_t)p.ctas;
     auto slot = [&](int k) -> int64_t {
       return first + (k == 0 ? 2 * (int64_t)c + 1 : 2 * (int64_t)(c + k)) * per;
     };
-    if (m.x > kMergeFew) merge_rows<D, 1, 8>(p, slot, m.x, sub, m.y, out0);
-    else merge_rows<D, kMergeAt, 2>(p, slot, m.x, sub * kMergeAt, m.y, out0);
+    const bool many = parts > kMergeFew;
+    const int row = many ? sub : sub * kMergeAt + (lane >> 3);
+    const bool real = row < rows;
+    float M = -INFINITY, l = 0.f, acc[4 * V];
+#pragma unroll
+    for (int e = 0; e < 4 * V; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int k = many ? lane : lane & 7; real && k < parts; k += many ? 32 : 8)
+      M = fmaxf(M, p.part_ml[slot(k) + row].x);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (many) {
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+    }
+    if (M == -INFINITY) M = 0.f;  // nothing at all, or nothing but NaN
+    const int step = many ? 4 : 1;
+#pragma unroll 1
+    for (int k = many ? lane >> 3 : 0; real && k < parts; k += 2 * step) {
+      float2 ml[2];
+      float4 x[2][V];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        if (k + f * step >= parts) break;
+        const int64_t at = slot(k + f * step) + row;
+        ml[f] = p.part_ml[at];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          x[f][e] = reinterpret_cast<const float4*>(p.part_o + at * D)[8 * e + (lane & 7)];
+      }
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        if (k + f * step >= parts) break;
+        if (ml[f].y == 0.f) continue;  // a part with nothing in it, whose o holds anything
+        const float w = ex2(ml[f].x - M);
+        l += w * ml[f].y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          acc[4 * e] += w * x[f][e].x;
+          acc[4 * e + 1] += w * x[f][e].y;
+          acc[4 * e + 2] += w * x[f][e].z;
+          acc[4 * e + 3] += w * x[f][e].w;
+        }
+      }
+    }
+    if (many) {
+#pragma unroll 1
+      for (int o = 8; o < 32; o <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+        for (int e = 0; e < 4 * V; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+      }
+    }
+    if (!real || (many && lane >= 8)) continue;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int G = p.Hq / p.Hkv;
+    const int64_t to = (out0 + (int64_t)(row / G) * p.Hq + row % G) * D + 4 * (lane & 7);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float4 y = make_float4(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv,
+                                   acc[4 * e + 3] * inv);
+      if (p.out_dtype == PKV_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + 32 * e) = y;
+      } else {
+        const bool bf = p.out_dtype == PKV_BF16;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to + 32 * e) =
+            make_uint2(bf ? pack2<true>(y.x, y.y) : pack2<false>(y.x, y.y),
+                       bf ? pack2<true>(y.z, y.w) : pack2<false>(y.z, y.w));
+      }
+    }
   }
 }
+
+static_assert(kMaxCtas >= kTreeMaxCtas, "the merge lists every share");
 
 template <bool BF16, int D>
 cudaError_t launch(const TreeLaunch& l) {
@@ -823,7 +827,7 @@ cudaError_t launch(const TreeLaunch& l) {
                        l.stream, l.p, l.tmap_q, l.tmap_k, l.tmap_v);
   if (e != cudaSuccess) return e;
   return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)(2 * l.p.ctas)),
-                          dim3(kMergeWarps * 32), 0, l.stream, l.p);
+                          dim3(kMergeThreads), 0, l.stream, l.p);
 }
 
 }  // namespace tr
