@@ -737,19 +737,19 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Tree
     const bool many = parts > kMergeFew;
     const int row = many ? sub : sub * kMergeAt + (lane >> 3);
     const bool real = row < rows;
+    // against a running maximum, so that m, l and o of a part are loaded together
     float M = -INFINITY, l = 0.f, acc[4 * V];
 #pragma unroll
     for (int e = 0; e < 4 * V; ++e) acc[e] = 0.f;
-#pragma unroll 1
-    for (int k = many ? lane : lane & 7; real && k < parts; k += many ? 32 : 8)
-      M = fmaxf(M, p.part_ml[slot(k) + row].x);
+    auto down = [&](float m2) -> float {  // to the new reference; the factor of a part at m2
+      const float top = fmaxf(M, m2), ref = top == -INFINITY ? 0.f : top;
+      const float w = ex2(M - ref);
+      M = top;
+      l *= w;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (many) {
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-    }
-    if (M == -INFINITY) M = 0.f;  // nothing at all, or nothing but NaN
+      for (int e = 0; e < 4 * V; ++e) acc[e] *= w;
+      return ex2(m2 - ref);
+    };
     const int step = many ? 4 : 1;
 #pragma unroll 1
     for (int k = many ? lane >> 3 : 0; real && k < parts; k += 2 * step) {
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Tree
       for (int f = 0; f < 2; ++f) {
         if (k + f * step >= parts) break;
         if (ml[f].y == 0.f) continue;  // a part with nothing in it, whose o holds anything
-        const float w = ex2(ml[f].x - M);
+        const float w = down(ml[f].x);
         l += w * ml[f].y;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -782,6 +782,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Tree
     if (many) {
 #pragma unroll 1
       for (int o = 8; o < 32; o <<= 1) {
+        down(__shfl_xor_sync(0xffffffffu, M, o));  // both lanes, to the same reference
         l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
         for (int e = 0; e < 4 * V; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
