@@ -99,47 +99,34 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
   __syncthreads();
 
   // ---- keys, and the positions of the rows that came since the last call; a
-  // thread takes four rows of a page at a time, kAhead of them in flight
-  constexpr int kAhead = 4;
-  for (int i0 = 4 * tid; i0 < cnt; i0 += 4 * NT * kAhead) {
-    float4 wq[kAhead];
-    int4 pq[kAhead];
+  // thread takes four rows of a page at a time
+#pragma unroll 1
+  for (int i = 4 * tid; i < cnt; i += 4 * NT) {
+    const int u = lo + i, first = rows[i / kPageSize], row = first + i % kPageSize;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 at = make_int4(0, 0, 0, 0);
+    if (first >= 0 && n > p.budget) w = *reinterpret_cast<const float4*>(p.weights + row);
+    if (first >= 0 && u < old) at = *reinterpret_cast<const int4*>(p.positions + row);
+    const float wv[4] = {w.x, w.y, w.z, w.w};
+    int pv[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + 4 * NT * a;
-      if (i >= cnt) break;
-      const int row = rows[i / kPageSize] + i % kPageSize;
-      const bool in = rows[i / kPageSize] >= 0;
-      if (in && n > p.budget) wq[a] = *reinterpret_cast<const float4*>(p.weights + row);
-      if (in && lo + i < old) pq[a] = *reinterpret_cast<const int4*>(p.positions + row);
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + 4 * NT * a, u = lo + i;
-      if (i >= cnt) break;
-      const int row = rows[i / kPageSize] + i % kPageSize;
-      const bool in = rows[i / kPageSize] >= 0;
-      const float wv[4] = {wq[a].x, wq[a].y, wq[a].z, wq[a].w};
-      int pv[4] = {pq[a].x, pq[a].y, pq[a].z, pq[a].w};
+    for (int e = 0; e < 4; ++e)
+      if (u + e >= old) pv[e] = told - n + u + e;
+    if (first >= 0 && u >= old && i + 4 <= cnt) {
+      *reinterpret_cast<int4*>(p.positions + row) = make_int4(pv[0], pv[1], pv[2], pv[3]);
+    } else if (first >= 0) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (u + e >= old) pv[e] = told - n + u + e;
-      if (in && u >= old && i + 4 <= cnt) {
-        *reinterpret_cast<int4*>(p.positions + row) = make_int4(pv[0], pv[1], pv[2], pv[3]);
-      } else if (in) {
+        if (u + e >= old && i + e < cnt) p.positions[row + e] = pv[e];
+    }
+    if (n <= p.budget) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (u + e >= old && i + e < cnt) p.positions[row + e] = pv[e];
-      }
-      if (n <= p.budget) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i + e >= cnt) break;
-        uint32_t key = 0;
-        if (in) key = pv[e] < p.sinks || pv[e] >= told - p.recent ? kGuarded : key_of(wv[e]);
-        keys[i + e] = key;
-        atomicAdd(&hist[key >> 24], 1u);
-      }
+    for (int e = 0; e < 4; ++e) {
+      if (i + e >= cnt) break;
+      uint32_t key = 0;
+      if (first >= 0) key = pv[e] < p.sinks || pv[e] >= told - p.recent ? kGuarded : key_of(wv[e]);
+      keys[i + e] = key;
+      atomicAdd(&hist[key >> 24], 1u);
     }
   }
   if (n <= p.budget) return;  // the same in every CTA of the cluster
@@ -305,51 +292,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
   // ---- the moves.  The lists become rows of the pool (-1: outside, nothing
   // moves); a thread takes the small things of a pair, whose loads are in flight
   // while K and V move.
-  struct Small {
-    int dst = -1, pos;
-    float w, s[2];
-  };
-  auto scale_at = [](int r, int e) -> int64_t {  // a page's 16 K scales, then its 16 V scales
-    return (r / kPageSize * (int64_t)2 + e) * kPageSize + r % kPageSize;
-  };
-  auto small_load = [&](int i, Small& x) {
-    const int u = from[i], src = row_of(u);
-    int dst = row_of(to[i]);
-    if (src < 0) dst = -1;
+#pragma unroll 1
+  for (int i = tid; i < mine; i += NT) {
+    const int u = from[i];
+    int dst = row_of(to[i]), src = row_of(u);
+    if (dst < 0 || src < 0) dst = src = -1;
     to[i] = dst;
     from[i] = src;
-    x.dst = dst;
-    if (dst < 0) return;
-    x.w = p.weights[src];
-    x.pos = u >= old ? told - n + u : p.positions[src];
+    if (src < 0) continue;
+    const float w = p.weights[src];
+    const int at = u >= old ? told - n + u : p.positions[src];
     if (p.scales != nullptr) {
-      x.s[0] = p.scales[scale_at(src, 0)];
-      x.s[1] = p.scales[scale_at(src, 1)];
+      // a page's 16 K scales, then its 16 V scales
+      const int64_t s0 = src + (int64_t)(src & ~(kPageSize - 1)), d0 = dst + (int64_t)(dst & ~(kPageSize - 1));
+      const float k = p.scales[s0], v = p.scales[s0 + kPageSize];
+      p.scales[d0] = k;
+      p.scales[d0 + kPageSize] = v;
     }
-  };
-  auto small_store = [&](const Small& x) {
-    if (x.dst < 0) return;
-    p.weights[x.dst] = x.w;
-    p.positions[x.dst] = x.pos;
-    if (p.scales != nullptr) {
-      p.scales[scale_at(x.dst, 0)] = x.s[0];
-      p.scales[scale_at(x.dst, 1)] = x.s[1];
-    }
-  };
-  Small first;
-  for (int i = tid; i < mine; i += NT) {
-    if (i == tid) {
-      small_load(i, first);
-    } else {
-      Small x;
-      small_load(i, x);
-      small_store(x);
-    }
+    p.weights[dst] = w;
+    p.positions[dst] = at;
   }
   __syncthreads();
   // K and V: 16 bytes per lane, a row's 2 cpr pieces side by side (a warp holds
   // one pair, or two of E4M3 and d 64), kAt steps in flight
-  constexpr int kAt = 8;
+  constexpr int kAt = 4;
   const int cpr = p.row_bytes >> 4;  // pieces of a row: 8 or 16
   const int wide = 16 / cpr;         // pairs per warp: 1 or 2
   const int sub = lane / (2 * cpr), piece = lane % (2 * cpr);
@@ -369,7 +335,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
     for (int e = 0; e < kAt; ++e)
       if (dst[e] >= 0) out[(int64_t)dst[e] * cpr] = data[e];
   }
-  small_store(first);
 }
 
 }  // namespace

@@ -229,3 +229,25 @@ def test_captured_and_replayed_with_other_lengths():
         for a, b in zip(c.pools(), want):
             assert torch.equal(a.reshape(-1), b.reshape(-1))
         assert c.new.tolist() == new
+
+
+@pytest.mark.parametrize("wider", [20000, 49133])
+def test_the_widest_tables(wider):
+    """Clusters of eight and of sixteen, most of whose CTAs have no row."""
+    c = Case([300, 90], [0, 0], [300, 90], seed=23, wider=wider)
+    c.check(128, 4, 16)
+
+
+def test_two_streams():
+    """Calls on pools of their own, queued side by side."""
+    cases = [Case([900 + 31 * i] * 6, [0] * 6, [900 + 31 * i] * 6, seed=25 + i) for i in range(2)]
+    wants = [c.expect(500, 4, 100) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for c, st in zip(cases, streams):
+        c.run(500, 4, 100, stream=st)
+    torch.cuda.synchronize()
+    for c, (want, new) in zip(cases, wants):
+        for a, b in zip(c.pools(), want):
+            assert torch.equal(a.reshape(-1), b.reshape(-1))
+        assert c.new.tolist() == new

@@ -297,3 +297,52 @@ def test_two_streams_with_a_workspace_each():
     for o, w in zip(outs, want):
         for x in o:
             assert torch.equal(x, w)
+
+
+def test_the_largest_batch():
+    """More sequences than the kernel keeps at hand, some of them empty or alone."""
+    g = torch.Generator().manual_seed(141)
+    B = 3840
+    nodes = torch.randint(0, 4, (B,), generator=g).tolist()
+    lens = [n + int(x) for n, x in zip(nodes, torch.randint(0, 20, (B,), generator=g))]
+    p = Paged(lens, 2, 1, 64, "f16", 142)
+    words = trees(nodes, 143)
+    q = p.queries(sum(nodes), 144, 2.0)
+    check(tree(p, q, nodes, words), *expect(p, q, nodes, words), "f32")
+    assert p.err.item() == 0
+
+
+def test_a_graph_whose_trees_and_lengths_change():
+    """Segments of one tile and of two, cut and whole, from one captured call."""
+    cap = [2500, 900, 300, 64]
+    p = Paged(cap, 16, 2, 128, "bf16", 151)
+    q = p.queries(200, 152, 2.0)
+    dq, o = q.cuda(), torch.empty(200, 16, 128, device="cuda")
+    starts = torch.zeros(5, dtype=torch.int32, device="cuda")
+    mask = torch.zeros(200, dtype=torch.int64, device="cuda")
+    ws = torch.full((pkv.pkv_tree_workspace_bytes(p.desc, 4, 64, p.mbs),), 0xff,
+                    dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        pkv.pkv_paged_tree_attention(p.desc, dq, p.kc, p.vc, p.tables, p.ctx, starts, 64, mask,
+                                     p.scale, o, ws)
+    K, V = p.K, p.V
+    for i, (nodes, lens) in enumerate([([64, 64, 64, 8], cap), ([3, 0, 17, 64], [2500, 5, 17, 64]),
+                                       ([16, 16, 16, 16], [16, 900, 129, 30]),
+                                       ([0, 0, 0, 1], [0, 1, 2, 1]), ([64, 1, 64, 1], cap)]):
+        words = trees(nodes, 153 + i)
+        n = sum(nodes)
+        p.ctx.copy_(torch.tensor(lens, dtype=torch.int32))
+        starts.copy_(starts_of(nodes))
+        mask[:n] = as_int64(words).cuda()
+        o.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        p.lens = lens
+        p.K, p.V = [k[:x] for k, x in zip(K, lens)], [v[:x] for v, x in zip(V, lens)]
+        ref, tol = expect(p, q[:n], nodes, words)
+        check(o[:n], ref, tol, "f32")
+        assert torch.all(o[n:] == 7.0)
+    assert p.err.item() == 0
