@@ -378,7 +378,7 @@ PKV_API size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t batc
  *   workspace     at least pkv_tree_workspace_bytes() bytes, 256-byte aligned,
  *                 not shared with calls that overlap.
  * 16-bit caches (E4M3 returns PKV_ERR_UNSUPPORTED, and so does a max_q_len above
- * PKV_MAX_TREE or a batch above 3840).  A sequence whose node count or length breaks the rules
+ * PKV_MAX_TREE or a batch above 3328).  A sequence whose node count or length breaks the rules
  * is a device-detected PKV_ERR_BOUNDS and its rows are not written.  A table
  * entry outside the pool is PKV_ERR_BOUNDS; its positions are left out, as by
  * pkv_paged_decode_attention.  Values (V) of nodes that some row of the tree

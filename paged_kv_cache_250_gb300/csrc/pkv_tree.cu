@@ -14,11 +14,11 @@
 // A segment wholly inside a share is normalised and written at once; one that is
 // cut leaves a partial in each share: slot 2 c where it came from the share
 // before, 2 c + 1 where it starts in share c.  Roles hand over through mbarriers:
-//   warps 0-3, 4-7  softmax of stream 0, 1: one row per thread, TMEM lane t;
-//   warps 8, 11     issue the MMAs; warps 9, 10 the tensor copies.
+//   warps 0-7, 8-15 softmax of stream 0, 1: a row is two threads';
+//   warps 16, 17    the tensor copies; warps 18, 19 issue the MMAs.
 // A stream is a row tile with its accumulator.
 //   Line 2, segments of two tiles: a share per CTA.  Both streams take every
-//   block, K and V double-buffered and copied by a warp each; warp 8 issues.
+//   block, K and V double-buffered and copied by a warp each; one warp issues.
 //   Line 1, segments of one tile (up to 128 rows: the usual tree), after it: a
 //   share per stream, with a K and a V buffer, a copying and an issuing warp of
 //   its own, so that one stream's segment ends, copies and products run under the
@@ -40,13 +40,14 @@ namespace tr {
 
 constexpr int kRows = kTreeRows, kTok = kTreeTok;
 constexpr int kPages = kTok / kPageSize;
-constexpr int kThreads = 384;
+constexpr int kThreads = 640, kSoft = 256;  // of them for each stream's softmax
 constexpr uint32_t kHalf = 16384;  // 128 rows x 128 bytes: 64 d columns of a tile or block
 // one barrier per buffer or stream, in pairs
 constexpr int kBarQ = 0, kBarQFree = 2, kBarKFull = 4, kBarVFull = 6, kBarKFree = 8,
               kBarVFree = 10, kBarSFull = 12, kBarPFull = 14, kBarODone = 16, kNumBars = 18;
 constexpr uint32_t kTmemCols = 512;  // S0/P0, S1/P1, then O0, O1
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kWarpCopy = 2 * kSoft / 32, kWarpMma = kWarpCopy + 2;  // two each
 constexpr int kSeqs = 128;  // sequences whose rows and lengths are at hand in shared memory
 
 template <int D>
@@ -54,7 +55,8 @@ struct Plan {
   static constexpr int NH = D / 64;
   static constexpr uint32_t kOffK = 2 * NH * kHalf;
   static constexpr uint32_t kOffV = 4 * NH * kHalf;
-  static constexpr uint32_t kOffBar = 6 * NH * kHalf;
+  static constexpr uint32_t kOffX = 6 * NH * kHalf;             // [2][2][2][128]: see softmax
+  static constexpr uint32_t kOffBar = kOffX + 4 * 8 * kRows;
   static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;     // TMEM base, abort, counts
   static constexpr uint32_t kOffSeq = (kOffMisc + 24 + 4 * kNumBars + 15) / 16 * 16;  // [kSeqs]
   static constexpr uint32_t kOffBounds = kOffSeq + 16 * kSeqs;  // [3]
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     for (int i = 0; i < kNumBars; ++i) {
       armed[i] = 0;
-      mbar_init(bar(i), (i == kBarPFull || i == kBarPFull + 1) ? kRows / 32 : 1);
+      mbar_init(bar(i), (i == kBarPFull || i == kBarPFull + 1) ? kSoft / 32 : 1);
     }
     fence_mbar_init();
     pfx[0] = 0;
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
-  if (warp == 9 || warp == 10) {
+  if (warp == kWarpCopy || warp == kWarpCopy + 1) {
     // ------------------------------------------------------------ copies
     bool ok = true;
     // uses of the buffers and Q slots so far: they give the barriers' phases
@@ -265,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return lane < kPages && j < wk.s.j0 + wk.s.nblk && pg < (wk.ctx + kPageSize - 1) / kPageSize
                  ? p.block_tables[(int64_t)wk.s.b * p.MBS + pg] : 0;
     };
-    const bool v = warp == 10;
-    begin(0);  // warp 9: Q and K, warp 10: V
+    const bool v = warp != kWarpCopy;
+    begin(0);  // the first warp: Q and K, the second: V
     while (ok && next()) {
       int cur = entry(wk.s.j0);
       for (int t = 0; ok && t < 2; ++t) {
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur = nxt;
       }
     }
-    const int t = warp - 9;
+    const int t = warp - kWarpCopy;
     begin(1 + t);  // each a stream
     while (ok && next()) {
       int cur = entry(wk.s.j0);
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur = nxt;
       }
     }
-  } else if (warp == 8 || warp == 11) {
+  } else if (warp >= kWarpMma) {
     // ------------------------------------------------------------ MMAs
     // blocks of each stream and uses of each buffer so far, segments so far
     uint32_t st = 0, u0 = 0, u1 = 0, segs = 0;
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) commit(kBarKFree + bb);
         if (q_last) commit(kBarQFree + t);
       };
-      // P_t: per 64 tokens 32 columns of hi pairs, then 32 of lo pairs
+      // P_t: per 16 tokens eight columns of hi pairs, then eight of lo pairs
       auto pv = [&](int t, int bb, bool add, bool last) {
         const uint64_t b0 = dv + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
         const uint32_t pt = tmem + (uint32_t)t * kTok;
@@ -329,9 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < kTok / 16; ++ks) {
           const uint64_t bv = b0 + ((uint32_t)ks * 16 * 128 >> 4);
-          const uint32_t pa = pt + (uint32_t)(ks >> 2) * 64 + (uint32_t)(ks & 3) * 8;
-          umma_ts(dt, pa, bv, kIdO, add || ks > 0);
-          umma_ts(dt, pa + 32, bv, kIdO, 1);
+          umma_ts(dt, pt + (uint32_t)ks * 16, bv, kIdO, add || ks > 0);
+          umma_ts(dt, pt + (uint32_t)ks * 16 + 8, bv, kIdO, 1);
         }
         commit(kBarODone + t);
         if (last) commit(kBarVFree + bb);
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         begin(0);
         while (ok && next()) {  // one buffer after the other, both streams from it
           const int n = wk.s.nblk;
-          if (warp == 8) {  // (warp 11 counts)
+          if (warp == kWarpMma) {  // (the other counts)
             uint32_t a0 = u0, a1 = u1;  // uses of the next block's buffer
             ok = wait(kBarKFull, a0 & 1) && wait(kBarQ, segs & 1) && wait(kBarQ + 1, segs & 1);
             if (!ok) break;
@@ -376,13 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++segs;
         }
       }
-      // Then a stream each, whose products are a chain.  Warp 11 begins when warp 8
-      // has issued all of line 2 (no earlier: a barrier's phases are told apart by
+      // Then a stream each, whose products are a chain.  The second warp begins when the
+      // first has issued all of line 2 (no earlier: a barrier's phases are told apart by
       // parity) and stream 1's last product of it, which is another thread's, is done.
       __syncwarp();
       asm volatile("bar.sync 1, 64;" ::: "memory");
       if (elect_one()) {  // the lane that was elected before
-        const int t = warp == 11;
+        const int t = warp != kWarpMma;
         uint32_t u = t ? u1 : u0;
         if (t == 1 && st > 0) {
           ok = wait(kBarODone + 1, (st - 1) & 1);
@@ -403,15 +404,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   } else {
     // ------------------------------------------------------------ softmax
-    const int t = warp >> 2;           // stream
-    const int tt = tid - t * kRows;    // row in the tile
+    // A row is two threads', of warps four apart: half 0 has tokens 0 to 63 of each
+    // block and the first half of O's columns, half 1 the others.
+    const int t = warp >> 3, half = (warp >> 2) & 1;  // stream, half
+    const int tt = (warp & 3) * 32 + lane;            // row in the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_sc = tmem + (uint32_t)t * kTok + lane_base;
-    const uint32_t t_o = tmem + 256 + (uint32_t)t * D + lane_base;
-    // 128 columns that hold nothing before the stream's first P is handed over
-    const uint32_t t_free = D == 64 ? tmem + 384 + lane_base : t_o;
+    const uint32_t t_sc = tmem + (uint32_t)t * kTok + 64 * half + lane_base;
+    const uint32_t t_o = tmem + 256 + (uint32_t)t * D + (uint32_t)half * (D / 2) + lane_base;
+    // 64 columns that hold nothing before the stream's first P is handed over
+    const uint32_t t_free = D == 64 ? tmem + 384 + 64 * half + lane_base : t_o;
+    float* const xch = reinterpret_cast<float*>(base_ptr + PL::kOffX) + t * 4 * kRows;
+    // What both threads of a row bring, and whether all of the two warps go on.  Two
+    // places in turn: nobody is more than one exchange ahead.
+    int turn = 0;
+    auto exchange = [&](float mine, bool good, float& its) -> bool {
+      float* at = xch + turn * 2 * kRows + tt;
+      turn ^= 1;
+      at[half * kRows] = mine;
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+          "barrier.cta.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(r) : "r"((uint32_t)good), "r"(2 + t * 4 + (warp & 3)) : "memory");
+      its = at[(half ^ 1) * kRows];
+      return r != 0;
+    };
     bool cold = true;
     const float c2 = p.scale_log2;
+    // A wait that gave up: the walk goes on for the exchanges, and nothing else.
     bool ok = true;
     int done = 0;            // blocks of the stream so far
     int u0 = 0, u1 = 0;      // uses of V's buffers so far
@@ -420,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int4 left = make_int4(0, 0, 0, 0), left_at = left;
     for (int ln = 0; ln < 2; ++ln) {  // line 2, then the stream's share of line 1
     begin(ln == 0 ? 0 : 1 + t);
-    while (ok && next()) {
+    while (next()) {
       const int nt = wk.s.nblk;
       int tok0 = wk.s.j0 * kTok;
       const int row = wk.s.row0 + (two ? t * kRows : 0) + tt;  // node x g + head
@@ -429,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int past = wk.ctx - wk.n;
       // the nodes that the row sees, and those that any row of the tree does
       const uint64_t nodes = wk.n == 64 ? ~0ull : (1ull << wk.n) - 1;
-      uint64_t mask = real ? (uint64_t)p.tree_mask[wk.q0 + row / G] & nodes : 0ull;
+      const uint64_t mask = real ? (uint64_t)p.tree_mask[wk.q0 + row / G] & nodes : 0ull;
       uint64_t any = lane < wk.n ? (uint64_t)p.tree_mask[wk.q0 + lane] : 0ull;
       if (lane + 32 < wk.n) any |= (uint64_t)p.tree_mask[wk.q0 + lane + 32];
       any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
@@ -441,117 +461,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       int i = cold ? -1 : 0;
       cold = false;
       if (i < 0) tok0 -= kTok;
-      for (; ok && i < nt; ++i, tok0 += kTok) {
+      for (; i < nt; ++i, tok0 += kTok) {
         const int kb = two ? i & 1 : t;  // the block's buffers, and their uses before
         const int ku = (kb ? u1 : u0) + (two ? i >> 1 : i);
         const uint32_t t_s = i < 0 ? t_free : t_sc;
         if (i >= 0) {
-          ok = __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
-          if (!ok) break;
+          ok = ok && __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
           tc_fence_after();
         }
         // a page outside the pool (reported by the copy warp, zeros in shared memory)
         // is left out: bit pg stands for the block's page pg
         const uint32_t bad = i < 0 ? 0 : bad_pages[2 * kb + (ku & 1)];
         if (busy) {
-        uint32_t sa[32], sb[32];
-        if (i >= 0 && (tok0 + kTok > past || bad != 0)) {  // scores that the row does not see
+          uint32_t sa[16], sb[16];
+          if (i >= 0 && (tok0 + kTok > past || bad != 0)) {  // scores that the row does not see
 #pragma unroll 1
-          for (int qq = 0; qq < 4; ++qq) {
-            // bit e: whether the row sees token tok0 + 32 qq + e
-            const int s = tok0 + 32 * qq - past;  // of the tree's node 0, negative in the past
-            uint32_t v = s <= -32 ? 0xffffffffu : s >= 64 ? 0u : s >= 0 ? (uint32_t)(mask >> s)
-                         : (uint32_t)(mask << -s) | ((1u << -s) - 1);
-            if ((bad >> (2 * qq)) & 1) v &= 0xffff0000u;
-            if ((bad >> (2 * qq + 1)) & 1) v &= 0x0000ffffu;
-            if (__all_sync(0xffffffffu, v == 0xffffffffu)) continue;
-            tmem_ld32(t_s + 32 * qq, sa);
+            for (int k = 0; k < 4; ++k) {  // a page
+              const int pg = 4 * half + k;
+              // bit e: whether the row sees token tok0 + 16 pg + e
+              const int s = tok0 + kPageSize * pg - past;  // of node 0, negative in the past
+              uint32_t v = s <= -16 ? 0xffffu : s >= 64 ? 0u : s >= 0 ? (uint32_t)(mask >> s)
+                           : (uint32_t)(mask << -s) | ((1u << -s) - 1);
+              if ((bad >> pg) & 1) v = 0;
+              if (__all_sync(0xffffffffu, (v & 0xffffu) == 0xffffu)) continue;
+              tmem_ld16_issue(t_s + 16 * k, sa);
+              tmem_ld16_wait(sa);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((v >> e) & 1)) sa[e] = 0xff800000u;  // -inf
-            tmem_st32(t_s + 32 * qq, sa);
-          }
-        }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto qmax = [&](const uint32_t (&sq)[32]) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            m4[e & 3] = max3(m4[e & 3], __uint_as_float(sq[2 * e]), __uint_as_float(sq[2 * e + 1]));
-        };
-        // quarters 3, 2, 1, 0: quarter 0 is still in sb when the P pass starts.  (Loops
-        // over two quarters, not four: the code is fetched once per launch.)
-        tmem_ld32_issue(t_s + 96, sa);
-        tmem_ld_wait(sa);
-        tmem_ld32_issue(t_s + 64, sb);
-        qmax(sa);
-        tmem_ld_wait(sb);
-        tmem_ld32_issue(t_s + 32, sa);
-        qmax(sb);
-        tmem_ld_wait(sa);
-        tmem_ld32_issue(t_s + 0, sb);
-        qmax(sa);
-        tmem_ld_wait(sb);
-        qmax(sb);
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
-        const bool grow = mx > m_ref + 8.f;  // lazy rescale, as in the prefill kernel
-        float alpha = 1.f;
-        if (grow) {
-          alpha = ex2(m_ref - mx);
-          m_ref = mx;
-          l_sum *= alpha;
-        }
-        if (i > 0) {
-          ok = __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + i - 1) & 1)));
-          if (!ok) break;
-          tc_fence_after();
-          if (__any_sync(0xffffffffu, grow)) {
-            uint32_t r[32];
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              tmem_ld32(t_o + (uint32_t)cc * 32, r);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-              tmem_st32(t_o + (uint32_t)cc * 32, r);
+              for (int e = 0; e < 16; ++e)
+                if (!((v >> e) & 1)) sa[e] = 0xff800000u;  // -inf
+              tmem_st16_issue(t_s + 16 * k, sa);
+              tmem_st_wait();
             }
           }
-        }
-        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t c2x2 = f2(c2, c2), nmu2 = f2(-mu, -mu);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t hi16[16], lo16[16];
-        auto qp = [&](const uint32_t (&sq)[32]) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto smax = [&](const uint32_t (&s)[16]) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = f2_split(fma2(f2(__uint_as_float(sq[2 * e]),
-                                              __uint_as_float(sq[2 * e + 1])), c2x2, nmu2));
-            const float p0 = ex2(y.x), p1 = ex2(y.y);
-            const uint64_t pp = f2(p0, p1);
-            acc[e & 3] = add2(acc[e & 3], pp);
-            hi16[e] = pack2<BF16>(p0, p1);
-            const float2 hf = unpack2<BF16>(hi16[e]);
-            const float2 l = f2_split(sub2(pp, f2(hf.x, hf.y)));
-            lo16[e] = pack2<BF16>(l.x, l.y);
+            for (int e = 0; e < 8; ++e)
+              m4[e & 3] = max3(m4[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+          };
+          // 16 tokens at a time, from the last: the first are still in sa when P's turn
+          // comes
+          tmem_ld16_issue(t_s + 48, sb);
+          tmem_ld16_wait(sb);
+          tmem_ld16_issue(t_s + 32, sa);
+          smax(sb);
+          tmem_ld16_wait(sa);
+          tmem_ld16_issue(t_s + 16, sb);
+          smax(sa);
+          tmem_ld16_wait(sb);
+          tmem_ld16_issue(t_s, sa);
+          smax(sb);
+          tmem_ld16_wait(sa);
+          smax(sa);
+          float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), its;
+          ok = exchange(mx, ok, its);
+          mx = fmaxf(mx, its) * c2;
+          const bool grow = mx > m_ref + 8.f;  // lazy rescale, as in the prefill kernel
+          float alpha = 1.f;
+          if (grow) {
+            alpha = ex2(m_ref - mx);
+            m_ref = mx;
+            l_sum *= alpha;
           }
-        };
-        // P of the first 32 tokens of half c / 64, then of the others
+          if (i > 0) {
+            ok = ok && __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + i - 1) & 1)));
+            tc_fence_after();
+            if (ok && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+              for (int cc = 0; cc < D / 64; ++cc) {
+                uint32_t r[32];
+                tmem_ld32(t_o + (uint32_t)cc * 32, r);
 #pragma unroll
-        for (uint32_t c = 0; c < 128; c += 64) {
-          tmem_ld32_issue(t_s + c + 32, sa);
-          qp(sb);
-          tmem_ld_wait(sa);
-          tmem_st16_issue(t_s + c, hi16);
-          tmem_st16_issue(t_s + c + 32, lo16);
-          if (c == 0) tmem_ld32_issue(t_s + 64, sb);
-          qp(sa);
-          if (c == 0) tmem_ld_wait(sb);
-          tmem_st16_issue(t_s + c + 16, hi16);
-          tmem_st16_issue(t_s + c + 48, lo16);
-        }
-        tmem_st_wait();
-        {
-          const float2 a0 = f2_split(add2(acc[0], acc[1])), a1 = f2_split(add2(acc[2], acc[3]));
-          l_sum += (a0.x + a0.y) + (a1.x + a1.y);
-        }
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                tmem_st32(t_o + (uint32_t)cc * 32, r);
+              }
+            }
+          }
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t c2x2 = f2(c2, c2), nmu2 = f2(-mu, -mu);
+          uint64_t acc[2] = {0ull, 0ull};
+          // P of 16 tokens over their scores: eight columns of hi pairs, eight of lo pairs
+          auto weigh = [&](const uint32_t (&s)[16], uint32_t c) {
+            uint32_t pq[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 y = f2_split(fma2(f2(__uint_as_float(s[2 * e]),
+                                                __uint_as_float(s[2 * e + 1])), c2x2, nmu2));
+              const float p0 = ex2(y.x), p1 = ex2(y.y);
+              const uint64_t pp = f2(p0, p1);
+              acc[e & 1] = add2(acc[e & 1], pp);
+              pq[e] = pack2<BF16>(p0, p1);
+              const float2 hf = unpack2<BF16>(pq[e]);
+              const float2 l = f2_split(sub2(pp, f2(hf.x, hf.y)));
+              pq[8 + e] = pack2<BF16>(l.x, l.y);
+            }
+            tmem_st16_issue(t_s + c, pq);
+          };
+          tmem_ld16_issue(t_s + 16, sb);
+          weigh(sa, 0);
+          tmem_ld16_wait(sb);
+          tmem_ld16_issue(t_s + 32, sa);
+          weigh(sb, 16);
+          tmem_ld16_wait(sa);
+          tmem_ld16_issue(t_s + 48, sb);
+          weigh(sa, 32);
+          tmem_ld16_wait(sb);
+          weigh(sb, 48);
+          tmem_st_wait();
+          const float2 a0 = f2_split(add2(acc[0], acc[1]));
+          l_sum += a0.x + a0.y;
         }
         if (i < 0) {
           m_ref = -INFINITY;
@@ -561,11 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // V rows behind the end, and of nodes that no row sees, may hold anything
         // (0 x NaN): zeroed in the staged block by the stream that uses it first
         if (tok0 + kTok > past && (t == 0 || !two)) {
-          ok = __all_sync(0xffffffffu, wait(kBarVFull + kb, (uint32_t)(ku & 1)));
-          if (!ok) break;
+          ok = ok && __all_sync(0xffffffffu, wait(kBarVFull + kb, (uint32_t)(ku & 1)));
           const int first = max(0, past - tok0);
           const uint32_t vb = base + kOffV + (uint32_t)kb * NH * kHalf;
-          for (int e = tt; e < (kTok - first) * 8 * NH; e += kRows) {
+          for (int e = half * kRows + tt; ok && e < (kTok - first) * 8 * NH; e += kSoft) {
             const int rr = first + e / (8 * NH), ch = e % (8 * NH), node = tok0 + rr - past;
             if (node < wk.n && ((any >> node) & 1)) continue;
             const uint32_t a = vb + (uint32_t)(ch >> 3) * kHalf + (uint32_t)rr * 128 +
@@ -577,25 +594,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPFull + t));
+        if (ok && lane == 0) mbar_arrive(bar(kBarPFull + t));
       }
       // ---- the part's end: the row's output, or the part's m, l and unnormalised o
-      if (ok)
-        ok = __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + nt - 1) & 1)));
+      ok = ok && __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + nt - 1) & 1)));
       done += nt;
       u0 += two ? (nt + 1) / 2 : nt;
       u1 += two ? nt / 2 : nt;
       const bool head = wk.s.j0 > 0, ends = wk.s.j0 + nt == wk.s.total, whole = !head && ends;
-      if (!whole) {
-        if (!head) {  // the shares that hold the rest follow this one
-          const int64_t cost = line[p.B];
-          left.x = (int)tree_share_of(wk.at - kTreeBlock, cost,
-                                      tree_shares(cost, two ? grid : 2 * grid)) - wk.share + 1;
-          left.y = min(two ? 2 * kRows : kRows, wk.n * G - wk.s.row0);
-          const int64_t o = (int64_t)(wk.q0 + wk.s.row0 / G) * p.Hq + wk.s.h * G;
-          left_at.x = (int)(o & 0xffffffff);
-          left_at.y = (int)(o >> 32);
-        }
+      if (!whole && !head) {  // the shares that hold the rest follow this one
+        const int64_t cost = line[p.B];
+        left.x = (int)tree_share_of(wk.at - kTreeBlock, cost,
+                                    tree_shares(cost, two ? grid : 2 * grid)) - wk.share + 1;
+        left.y = min(two ? 2 * kRows : kRows, wk.n * G - wk.s.row0);
+        const int64_t o = (int64_t)(wk.q0 + wk.s.row0 / G) * p.Hq + wk.s.h * G;
+        left_at.x = (int)(o & 0xffffffff);
+        left_at.y = (int)(o >> 32);
+      }
+      if (busy) {
+        float its;
+        ok = exchange(l_sum, ok, its);
+        l_sum = half == 0 ? l_sum + its : its + l_sum;  // the same sum in both
       }
       if (ok && busy) {
         tc_fence_after();
@@ -604,13 +623,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                              (two ? t * kRows : 4 * kRows * (int64_t)grid) + tt;
         const float inv = some ? 1.f / l_sum : 0.f;
         const int64_t orow = (int64_t)(wk.q0 + row / G) * p.Hq + wk.s.h * G + row % G;
-        if (!whole && real)
+        if (!whole && real && half == 0)
           p.part_ml[prow] = some ? make_float2(m_ref, l_sum) : make_float2(-INFINITY, 0.f);
 #pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
+        for (int cc = 0; cc < D / 64; ++cc) {
           uint32_t r[32];
           tmem_ld32(t_o + (uint32_t)cc * 32, r);
           if (!real) continue;
+          const int col = half * (D / 2) + cc * 32;
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
@@ -621,16 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float x = __uint_as_float(r[2 * e]), y = __uint_as_float(r[2 * e + 1]);
                 r[e] = bf ? pack2<true>(x, y) : pack2<false>(x, y);
               }
-              uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D +
-                                                   cc * 32);
+              uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D + col);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
               continue;
             }
           }
-          float* po = whole ? static_cast<float*>(p.out) + orow * D + cc * 32
-                            : p.part_o + prow * D + cc * 32;
+          float* po = whole ? static_cast<float*>(p.out) + orow * D + col
+                            : p.part_o + prow * D + col;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             reinterpret_cast<uint4*>(po)[e] =
@@ -639,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();  // O_t is read before P_t of the next part is handed over
       }
     }
-    if (tt == 0 && (ln == 1 || t == 0)) {
+    if (tt == 0 && half == 0 && (ln == 1 || t == 0)) {
       int4* meta = p.meta + 2 * (ln == 0 ? wk.share : grid + wk.share);
       meta[0] = left;
       meta[1] = left_at;

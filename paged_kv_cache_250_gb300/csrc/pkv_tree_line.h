@@ -17,7 +17,7 @@ namespace pkv {
 constexpr int kTreeRows = 128, kTreeTok = 128;  // rows of a tile, tokens of a block
 constexpr int kTreeBlock = 2, kTreeSeg = 4;
 constexpr int kTreeMinShare = 4;  // a share is worth at least this much
-constexpr int kTreeMaxBatch = 3840, kTreeMaxCtas = 256;
+constexpr int kTreeMaxBatch = 3328, kTreeMaxCtas = 256;
 static_assert(kTreeMinShare >= kTreeBlock, "no share without a block inside a segment");
 
 PKV_HD int tree_blocks(int ctx) { return (int)(((int64_t)ctx + kTreeTok - 1) / kTreeTok); }

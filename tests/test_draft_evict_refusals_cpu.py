@@ -34,7 +34,7 @@ def tree(x=None, q=F, kc=F, vc=F, tab=F, ctx=F, starts=F, B=2, total=8, most=4, 
     (dict(mask=ctypes.c_void_p(0x10004)), INV), (dict(starts=ODD), INV),
     (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV),
     (dict(scale=float("inf")), INV), (dict(B=-1), INV), (dict(total=-1), INV),
-    (dict(most=-1), INV), (dict(most=65), UNS), (dict(mbs=0), INV), (dict(B=3841), UNS),
+    (dict(most=-1), INV), (dict(most=65), UNS), (dict(mbs=0), INV), (dict(B=3329), UNS),
     (dict(qt=pkv.PKV_F16), INV), (dict(ot=pkv.PKV_FP8_E4M3), UNS),
     (dict(x=desc(dtype=pkv.PKV_FP8_E4M3)), UNS), (dict(x=desc(dtype=pkv.PKV_FP8_E4M3_TOKEN)), UNS),
     (dict(x=desc(d=96)), UNS), (dict(x=desc(page=32)), UNS), (dict(x=desc(Hq=6)), UNS),

@@ -302,7 +302,7 @@ def test_two_streams_with_a_workspace_each():
 def test_the_largest_batch():
     """More sequences than the kernel keeps at hand, some of them empty or alone."""
     g = torch.Generator().manual_seed(141)
-    B = 3840
+    B = 3328
     nodes = torch.randint(0, 4, (B,), generator=g).tolist()
     lens = [n + int(x) for n, x in zip(nodes, torch.randint(0, 20, (B,), generator=g))]
     p = Paged(lens, 2, 1, 64, "f16", 142)
