@@ -78,6 +78,13 @@ __device__ __forceinline__ bool seq_of(const TreeParams& p, int b, int& q0, int&
   return false;
 }
 
+// 32 bytes at once: a whole sector
+__device__ __forceinline__ void store32(void* to, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmq,
@@ -631,29 +638,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(t_o + (uint32_t)cc * 32, r);
           if (!real) continue;
           const int col = half * (D / 2) + cc * 32;
-          if (whole) {
+          if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
-            if (p.out_dtype != PKV_F32) {
-              const bool bf = p.out_dtype == PKV_BF16;
+            for (int e = 0; e < 4; ++e) store32(p.part_o + prow * D + col + 8 * e, r + 8 * e);
+            continue;
+          }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float x = __uint_as_float(r[2 * e]), y = __uint_as_float(r[2 * e + 1]);
-                r[e] = bf ? pack2<true>(x, y) : pack2<false>(x, y);
-              }
-              uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D + col);
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+          uint4* to;  // (the output need not be aligned to whole sectors)
+          if (p.out_dtype == PKV_F32) {
+            to = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + orow * D + col);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-              continue;
+            for (int e = 4; e < 8; ++e)
+              to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          } else {
+            to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D + col);
+            const bool bf = p.out_dtype == PKV_BF16;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = __uint_as_float(r[2 * e]), y = __uint_as_float(r[2 * e + 1]);
+              r[e] = bf ? pack2<true>(x, y) : pack2<false>(x, y);
             }
           }
-          float* po = whole ? static_cast<float*>(p.out) + orow * D + col
-                            : p.part_o + prow * D + col;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint4*>(po)[e] =
-                make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          for (int e = 0; e < 4; ++e)
+            to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
         }
         tc_fence_before();  // O_t is read before P_t of the next part is handed over
       }
