@@ -4,8 +4,12 @@
 // The decode kernel leaves every score x (log2 units) and, per query head, the
 // logarithm of the row's sum (lse = m + log2 l).  A row's new weight is
 //   w = decay w + sum over the g query heads of the KV head of 2^(x - lse).
-// Bound by HBM and the launch: per row 4 g bytes of scores, most still in L2,
-// and its weight read and written.
+// Bound by latency, and by HBM for large batches: per row 4 g bytes of scores, part
+// of them still in L2, and its weight read and written.  The call takes 57.6 us for 32
+// sequences of up to 4096 tokens (the plain decode 50.7, the decode kernel alone in
+// this form 51 and 1.5 for its stores), 235 for 64 of 8192 tokens in a per-token E4M3
+// cache (202; 67 MB of scores).  Four rows per thread with wide loads made no difference
+// to either, nor did dropping the scores' lines from L2 once read (231).
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 

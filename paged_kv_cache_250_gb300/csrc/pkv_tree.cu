@@ -24,8 +24,24 @@
 //   its own, so that one stream's segment ends, copies and products run under the
 //   other's softmax.
 //   S = Q K^T   tcgen05.mma M 128 x N 128 x K d from shared memory;
-//   P           hi + lo 16-bit pairs over S in tensor memory;
+//   P           hi + lo 16-bit pairs over S in tensor memory (the weights keep
+//               about 16 bits, as in the framework's other attention kernels);
 //   O += P V    tcgen05.mma with A from tensor memory, twice per 16 tokens.
+// One tile is bound by HBM: 8 x 32768 tokens of 8 KV heads and 8 nodes, 1.07 GB, 180
+// us, 6.0 TB/s (235 us while one warp copied K and V of both streams in turn: it
+// waited for one stream's buffer while the other's was free).  Two tiles are bound by
+// each stream's chain of softmax (2300 cycles per block) and products (2200): 274 us
+// for the same cache and 64 nodes, 1.0 PFLOP/s counted, 1.5 with the second product
+// of P; the tensor pipe is active 64 % of the cycles.  Short segments and small calls
+// are bound by latency: 64 sequences of 512 tokens 46 us, of 128 tokens 20, one of 708
+// tokens 13.7, of which 4 are the merge behind.  A launch fetches its code anew, so
+// short code counts: scores masked in tensor memory before the softmax, instead of a
+// second softmax with masks, and one copy of it for both lines took a cold launch of
+// the smallest call from 24 to 15 us.
+// Measured and not kept: both streams on one segment with a join at its end (tree of
+// 32 ragged sequences 120 us, now 93); K and V prefetched into L2 by the copy warp
+// (176 -> 290 us: its look-ups held up its copies); P handed over in two halves (280
+// -> 277, ragged trees 97 -> 102); 32 scores at a time (280 -> 289).
 //
 // tree_merge_kernel joins the parts of the cut segments, in order.
 #include <atomic>
