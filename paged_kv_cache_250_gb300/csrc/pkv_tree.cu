@@ -306,6 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur = nxt;
       }
     }
+    // The second warp goes on to stream 1's line when the first has issued all of line
+    // 2: it never waited for Q's slots, and phases are told apart by parity only while
+    // at most one is outstanding.
+    __syncwarp();
+    asm volatile("bar.sync 10, 64;" ::: "memory");
     const int t = warp - kWarpCopy;
     begin(1 + t);  // each a stream
     while (ok && next()) {
