@@ -374,7 +374,7 @@ PKV_API size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t batc
  *                 sees no position at all gets a zero output row.
  *   scale         > 0 (the softmax scale).
  *   out           [total_q][num_q_heads][head_dim] of out_dtype (F16 | BF16 |
- *                 F32).
+ *                 F32).  Must not alias inputs.
  *   workspace     at least pkv_tree_workspace_bytes() bytes, 256-byte aligned,
  *                 not shared with calls that overlap.
  * 16-bit caches (E4M3 returns PKV_ERR_UNSUPPORTED, and so does a max_q_len above

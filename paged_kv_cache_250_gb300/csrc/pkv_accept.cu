@@ -15,11 +15,10 @@ constexpr int kAcceptThreads = 128;
 static_assert(2 * kMaxPath <= kAcceptThreads, "a thread per step and per scale");
 
 __global__ void __launch_bounds__(kAcceptThreads) accept_path_kernel(const AcceptParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv, tid = threadIdx.x;
   extern __shared__ uint4 stage[];                // [max_path][K row, V row]
   __shared__ int32_t src_row[kMaxPath], dst_row[kMaxPath];  // of the pool; -1: nothing moves
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  griddep_wait_then_trigger();
   const int node = tid < p.max_path ? p.path[(int64_t)b * p.max_path + tid] : 0;
   const int ctx = p.context_lens[b], n = p.q_start[b + 1] - p.q_start[b], len = p.path_lens[b];
   if (ctx < 0 || ctx > p.MBS * kPageSize || n < 0 || n > ctx || len < 0 || len > n ||

@@ -735,11 +735,10 @@ pkv_status pkv_paged_decode_attention_scored(
   form.mode = pkv::kModeScored;
   form.lse = reinterpret_cast<float*>(ws);
   form.scores = reinterpret_cast<float*>(ws + s.scores);
-  // the weights kernel may be launched while the decode kernel runs
+  // (the kernel itself lets the weights kernel start while it runs)
   st = decode_impl(desc, q, k_cache, v_cache, block_tables, context_lens, batch,
                    max_blocks_per_seq, max_context_len_hint, scale, out, q_dtype, out_dtype, own,
-                   own_bytes, stream, /*early_prologue=*/0, 1, 0, 0, nullptr, nullptr, PKV_BF16,
-                   /*trigger_next=*/1, form);
+                   own_bytes, stream, /*early_prologue=*/0, 1, 0, 0, nullptr, nullptr, PKV_BF16, 0, form);
   if (st != PKV_OK || batch == 0) return st;
   pkv::WeightParams w;
   w.scores = form.scores;

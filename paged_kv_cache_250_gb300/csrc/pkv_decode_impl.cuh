@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
-  if (!p.early_prologue) griddep_wait();
+  if constexpr (kScored) griddep_wait_then_trigger();
+  else if (!p.early_prologue) griddep_wait();
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);

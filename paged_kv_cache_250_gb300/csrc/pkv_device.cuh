@@ -17,6 +17,16 @@ __device__ __forceinline__ void report_error(int32_t* err_word, int32_t code) {
   if (err_word != nullptr) atomicCAS(err_word, 0, code);
 }
 
+// ---------------------------------------------------------------- kernels in a row
+// Wait for the kernel in front, then let the next one start its prologue.  In this
+// order whatever starts behind finds all kernels but the last complete: a step may
+// read lengths that an earlier kernel wrote while the one in front still runs
+// (PKV_STEP_OVERLAP).
+__device__ __forceinline__ void griddep_wait_then_trigger() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- smem addr
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

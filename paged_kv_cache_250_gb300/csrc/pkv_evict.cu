@@ -64,7 +64,6 @@ constexpr size_t smem_of(int64_t rows, int cl) {
 template <int CL, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams p) {
   constexpr int NW = NT / 32;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t* hist = smem;                       // [kDigits][kBins]
   uint32_t* warp_a = hist + kDigits * kBins;   // [NW] counts of the warps
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
     else return x;
   };
   for (int i = tid; i < kDigits * kBins; i += NT) hist[i] = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  griddep_wait_then_trigger();
   const int n = p.context_lens[b], old = p.old_lens[b], told = p.num_tokens[b];
   if (n < 0 || n > p.MBS * kPageSize || old < 0 || old > n || told < n) {
     if (h == 0 && rank == 0 && tid == 0) report_error(p.err_word, PKV_ERR_BOUNDS);

@@ -19,10 +19,9 @@ constexpr int kWeightThreads = 256;
 
 template <int G>
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int seg = blockIdx.x / p.splits, sub = blockIdx.x - seg * p.splits;
   const int b = seg / p.Hkv, h = seg - b * p.Hkv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  griddep_wait_then_trigger();
   const int ctx = p.context_lens[b];
   if (ctx < 0 || ctx > p.MBS * kPageSize) return;  // reported by the decode kernel
   float lse[G];

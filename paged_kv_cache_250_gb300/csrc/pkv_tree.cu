@@ -140,8 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pfx[p.B + 1] = 0;
   }
   // so far nothing of the kernel in front was needed, and it may still run
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  griddep_wait_then_trigger();
   // Tensor memory is taken behind the wait, never before it: a kernel in front
   // that lets this one start may have yet to take its own on the same SM.
   if (warp == 0) {
@@ -728,8 +727,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Tree
   __shared__ int upto[kMergeShares];   // groups up to and with a cut segment
   __shared__ int4 cut[kMergeShares];   // its entry of meta, parts and rows, first output row
   __shared__ int warp_n[kMergeWarps], warp_g[kMergeWarps];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  griddep_wait_then_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int cuts = 0, groups = 0;
   for (int i0 = 0; i0 < 3 * p.ctas; i0 += kMergeThreads) {
