@@ -30,7 +30,7 @@
 // One tile is bound by HBM: 8 x 32768 tokens of 8 KV heads and 8 nodes, 1.07 GB, 180
 // us, 6.0 TB/s (235 us while one warp copied K and V of both streams in turn: it
 // waited for one stream's buffer while the other's was free).  Two tiles are bound by
-// each stream's chain of softmax (2300 cycles per block) and products (2200): 274 us
+// each stream's chain of softmax (2200 cycles per block) and products (2200): 266 us
 // for the same cache and 64 nodes, 1.0 PFLOP/s counted, 1.5 with the second product
 // of P; the tensor pipe is active 64 % of the cycles.  Short segments and small calls
 // are bound by latency: 64 sequences of 512 tokens 46 us, of 128 tokens 20, one of 708
@@ -39,9 +39,10 @@
 // second softmax with masks, and one copy of it for both lines took a cold launch of
 // the smallest call from 24 to 15 us.
 // Measured and not kept: both streams on one segment with a join at its end (tree of
-// 32 ragged sequences 120 us, now 93); K and V prefetched into L2 by the copy warp
+// 32 ragged sequences 120 us, now 90); K and V prefetched into L2 by the copy warp
 // (176 -> 290 us: its look-ups held up its copies); P handed over in two halves (280
-// -> 277, ragged trees 97 -> 102); 32 scores at a time (280 -> 289).
+// -> 277, ragged trees 97 -> 102); 32 scores at a time (280 -> 289); a quarter of the
+// powers of two as a polynomial on the FMA pipe (280 -> 296).
 //
 // tree_merge_kernel joins the parts of the cut segments, in order.
 #include <atomic>
@@ -99,6 +100,16 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// a 16-bit pair in fp32; bf16 in an instruction each (the conversion functions took
+// 59 more per warp and block: 274 us for 8 x 32768 tokens and 64 nodes, now 266)
+template <bool BF16>
+__device__ __forceinline__ float2 floats_of(uint32_t u) {
+  if constexpr (BF16)
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  else
+    return unpack2<false>(u);
 }
 
 template <bool BF16, int D>
@@ -462,11 +473,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int done = 0;            // blocks of the stream so far
     int u0 = 0, u1 = 0;      // uses of V's buffers so far
-    // what the share leaves for the merge: parts (0: nothing), rows; the output row of
-    // the first (as two words)
-    int4 left = make_int4(0, 0, 0, 0), left_at = left;
     for (int ln = 0; ln < 2; ++ln) {  // line 2, then the stream's share of line 1
     begin(ln == 0 ? 0 : 1 + t);
+    // what the share leaves for the merge, if anything, is its last part
+    const bool tells = tt == 0 && half == 0 && (ln == 1 || t == 0);
+    if (tells) p.meta[2 * (ln == 0 ? wk.share : grid + wk.share)] = make_int4(0, 0, 0, 0);
     while (next()) {
       const int nt = wk.s.nblk;
       int tok0 = wk.s.j0 * kTok;
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t pp = f2(p0, p1);
               acc[e & 1] = add2(acc[e & 1], pp);
               pq[e] = pack2<BF16>(p0, p1);
-              const float2 hf = unpack2<BF16>(pq[e]);
+              const float2 hf = floats_of<BF16>(pq[e]);
               const float2 l = f2_split(sub2(pp, f2(hf.x, hf.y)));
               pq[8 + e] = pack2<BF16>(l.x, l.y);
             }
@@ -629,14 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       u0 += two ? (nt + 1) / 2 : nt;
       u1 += two ? nt / 2 : nt;
       const bool head = wk.s.j0 > 0, ends = wk.s.j0 + nt == wk.s.total, whole = !head && ends;
-      if (!whole && !head) {  // the shares that hold the rest follow this one
+      if (tells && !whole && !head) {  // the shares that hold the rest follow this one
         const int64_t cost = line[p.B];
-        left.x = (int)tree_share_of(wk.at - kTreeBlock, cost,
-                                    tree_shares(cost, two ? grid : 2 * grid)) - wk.share + 1;
-        left.y = min(two ? 2 * kRows : kRows, wk.n * G - wk.s.row0);
+        const int parts = (int)tree_share_of(wk.at - kTreeBlock, cost,
+                                             tree_shares(cost, two ? grid : 2 * grid)) - wk.share + 1;
         const int64_t o = (int64_t)(wk.q0 + wk.s.row0 / G) * p.Hq + wk.s.h * G;
-        left_at.x = (int)(o & 0xffffffff);
-        left_at.y = (int)(o >> 32);
+        // parts, rows; the output row of the first
+        int4* const meta = p.meta + 2 * (ln == 0 ? wk.share : grid + wk.share);
+        meta[0] = make_int4(parts, min(two ? 2 * kRows : kRows, wk.n * G - wk.s.row0), 0, 0);
+        meta[1] = make_int4((int)(o & 0xffffffff), (int)(o >> 32), 0, 0);
       }
       if (busy) {
         float its;
@@ -687,12 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();  // O_t is read before P_t of the next part is handed over
       }
     }
-    if (tt == 0 && half == 0 && (ln == 1 || t == 0)) {
-      int4* meta = p.meta + 2 * (ln == 0 ? wk.share : grid + wk.share);
-      meta[0] = left;
-      meta[1] = left_at;
-    }
-    left.x = 0;
     }
   }
 
