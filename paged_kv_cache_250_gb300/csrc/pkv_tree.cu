@@ -30,16 +30,16 @@
 // One tile is bound by HBM: 8 x 32768 tokens of 8 KV heads and 8 nodes, 1.07 GB, 180
 // us, 6.0 TB/s (235 us while one warp copied K and V of both streams in turn: it
 // waited for one stream's buffer while the other's was free).  Two tiles are bound by
-// each stream's chain of softmax (2200 cycles per block) and products (2200): 266 us
+// each stream's chain of softmax (2200 cycles per block) and products (2200): 264 us
 // for the same cache and 64 nodes, 1.0 PFLOP/s counted, 1.5 with the second product
-// of P; the tensor pipe is active 64 % of the cycles.  Short segments and small calls
-// are bound by latency: 64 sequences of 512 tokens 46 us, of 128 tokens 20, one of 708
-// tokens 13.7, of which 4 are the merge behind.  A launch fetches its code anew, so
+// of P; the tensor pipe is active 70 % of the cycles.  Short segments and small calls
+// are bound by latency: 64 sequences of 512 tokens 44 us, of 128 tokens 20, one of 708
+// tokens 13.3, of which 4 are the merge behind.  A launch fetches its code anew, so
 // short code counts: scores masked in tensor memory before the softmax, instead of a
 // second softmax with masks, and one copy of it for both lines took a cold launch of
 // the smallest call from 24 to 15 us.
 // Measured and not kept: both streams on one segment with a join at its end (tree of
-// 32 ragged sequences 120 us, now 90); K and V prefetched into L2 by the copy warp
+// 32 ragged sequences 120 us, now 88); K and V prefetched into L2 by the copy warp
 // (176 -> 290 us: its look-ups held up its copies); P handed over in two halves (280
 // -> 277, ragged trees 97 -> 102); 32 scores at a time (280 -> 289); a quarter of the
 // powers of two as a polynomial on the FMA pipe (280 -> 296).
@@ -485,13 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool real = row < wk.n * G;
       const bool busy = row - lane < wk.n * G;  // a warp without rows only keeps the barriers
       const int past = wk.ctx - wk.n;
-      // the nodes that the row sees, and those that any row of the tree does
-      const uint64_t nodes = wk.n == 64 ? ~0ull : (1ull << wk.n) - 1;
-      const uint64_t mask = real ? (uint64_t)p.tree_mask[wk.q0 + row / G] & nodes : 0ull;
-      uint64_t any = lane < wk.n ? (uint64_t)p.tree_mask[wk.q0 + lane] : 0ull;
-      if (lane + 32 < wk.n) any |= (uint64_t)p.tree_mask[wk.q0 + lane + 32];
-      any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
-             __reduce_or_sync(0xffffffffu, (uint32_t)any)) & nodes;
+      uint64_t mask = 0, any = 0;  // the nodes that the row sees, and that any row does
       float m_ref = -INFINITY, l_sum = 0.f;
       // The first part begins with a step on whatever lies in columns that no product
       // uses yet, and drops what comes out: it brings the instructions into the cache
@@ -503,6 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kb = two ? i & 1 : t;  // the block's buffers, and their uses before
         const int ku = (kb ? u1 : u0) + (two ? i >> 1 : i);
         const uint32_t t_s = i < 0 ? t_free : t_sc;
+        if (i >= 0 && tok0 + kTok > past && (i == 0 || tok0 <= past)) {
+          // the first block with nodes: their words come while the scores are on their
+          // way (at the part's start they waited behind the last part's stores, 3000
+          // cycles: ragged trees 90.5 us, now 88)
+          const uint64_t nodes = wk.n == 64 ? ~0ull : (1ull << wk.n) - 1;
+          if (real) mask = (uint64_t)p.tree_mask[wk.q0 + row / G] & nodes;
+          any = lane < wk.n ? (uint64_t)p.tree_mask[wk.q0 + lane] : 0ull;
+          if (lane + 32 < wk.n) any |= (uint64_t)p.tree_mask[wk.q0 + lane + 32];
+          any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
+                 __reduce_or_sync(0xffffffffu, (uint32_t)any)) & nodes;
+        }
         if (i >= 0) {
           ok = ok && __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
           tc_fence_after();
