@@ -30,16 +30,16 @@
 // One tile is bound by HBM: 8 x 32768 tokens of 8 KV heads and 8 nodes, 1.07 GB, 180
 // us, 6.0 TB/s (235 us while one warp copied K and V of both streams in turn: it
 // waited for one stream's buffer while the other's was free).  Two tiles are bound by
-// each stream's chain of softmax (2200 cycles per block) and products (2200): 264 us
-// for the same cache and 64 nodes, 1.0 PFLOP/s counted, 1.5 with the second product
+// each stream's chain of softmax (2200 cycles per block) and products (2200): 263 us
+// for the same cache and 64 nodes, 1.0 PFLOP/s counted, 1.6 with the second product
 // of P; the tensor pipe is active 70 % of the cycles.  Short segments and small calls
-// are bound by latency: 64 sequences of 512 tokens 44 us, of 128 tokens 20, one of 708
-// tokens 13.3, of which 4 are the merge behind.  A launch fetches its code anew, so
+// are bound by latency: 64 sequences of 512 tokens 42 us, of 128 tokens 20, one of 708
+// tokens 12.6, of which 3 are the merge behind.  A launch fetches its code anew, so
 // short code counts: scores masked in tensor memory before the softmax, instead of a
 // second softmax with masks, and one copy of it for both lines took a cold launch of
 // the smallest call from 24 to 15 us.
 // Measured and not kept: both streams on one segment with a join at its end (tree of
-// 32 ragged sequences 120 us, now 88); K and V prefetched into L2 by the copy warp
+// 32 ragged sequences 120 us, now 83); K and V prefetched into L2 by the copy warp
 // (176 -> 290 us: its look-ups held up its copies); P handed over in two halves (280
 // -> 277, ragged trees 97 -> 102); 32 scores at a time (280 -> 289); a quarter of the
 // powers of two as a polynomial on the FMA pipe (280 -> 296).
@@ -111,6 +111,16 @@ __device__ __forceinline__ float2 floats_of(uint32_t u) {
   else
     return unpack2<false>(u);
 }
+
+// Partial rows lie in groups of 32, eight columns of each row after the other: what a
+// warp stores at once (a piece of each lane's row) is contiguous, where rows of their
+// own took a line per lane (64 nodes behind 701 tokens 17.5 us, now 16.4).  A row's
+// first piece, and the steps to the next:
+template <int D>
+__device__ __forceinline__ int64_t part_at(int64_t row) {
+  return (row & ~31ll) * D + (row & 31) * 8;
+}
+constexpr int kPartStep = 32 * 8;
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -500,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i >= 0 && tok0 + kTok > past && (i == 0 || tok0 <= past)) {
           // the first block with nodes: their words come while the scores are on their
           // way (at the part's start they waited behind the last part's stores, 3000
-          // cycles: ragged trees 90.5 us, now 88)
+          // cycles: ragged trees 90.5 us, then 88)
           const uint64_t nodes = wk.n == 64 ? ~0ull : (1ull << wk.n) - 1;
           if (real) mask = (uint64_t)p.tree_mask[wk.q0 + row / G] & nodes;
           any = lane < wk.n ? (uint64_t)p.tree_mask[wk.q0 + lane] : 0ull;
@@ -665,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool some = l_sum != 0.f;  // NaN counts: it has to show
         const int64_t prow = (2 * (int64_t)wk.share + (head ? 0 : 1)) * (two ? 2 * kRows : kRows) +
                              (two ? t * kRows : 4 * kRows * (int64_t)grid) + tt;
+        float* const po = p.part_o + part_at<D>(prow) + half * (D / 16) * kPartStep;
         const float inv = some ? 1.f / l_sum : 0.f;
         const int64_t orow = (int64_t)(wk.q0 + row / G) * p.Hq + wk.s.h * G + row % G;
         if (!whole && real && half == 0)
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = half * (D / 2) + cc * 32;
           if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store32(p.part_o + prow * D + col + 8 * e, r + 8 * e);
+            for (int e = 0; e < 4; ++e) store32(po + (4 * cc + e) * kPartStep, r + 8 * e);
             continue;
           }
 #pragma unroll
@@ -724,17 +735,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- the merge of the segments that share boundaries cut.  Every CTA lists them
 // (their groups of rows, summed up) and its warps take every grid-th group.  Eight
 // lanes hold a row's columns: a warp joins four rows of a segment with few parts, or
-// the parts of one row of a segment with many, every fourth in eight lanes.  Bound
-// by latency: the launch, a round of loads, and the code, which is fetched anew by
-// every launch and therefore short (four rows per warp and lane unrolled took 22 us
-// for 35 MB of partials).
+// the parts of one row of a segment with many, every fourth in eight lanes; four parts
+// are in flight per lane.  Bound by latency: the launch, a round of loads, and the code,
+// which is fetched anew by every launch and therefore short (four rows per warp and lane
+// unrolled took 22 us for 35 MB of partials).  One CTA per SM, so that a thread has 128
+// registers: two with 64, whose loads spilled, took ragged trees of 32 sequences from 83
+// to 87.5 us and one sequence of 32768 tokens from 36 to 42.
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeAt = 4, kMergeFew = 4;
 constexpr int kMergeShares = 768;  // room for the shares of both lines
 constexpr int kMaxCtas = kMergeShares / 3;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 1) tree_merge_kernel(const TreeParams p) {
   __shared__ int upto[kMergeShares];   // groups up to and with a cut segment
   __shared__ int4 cut[kMergeShares];   // its entry of meta, parts and rows, first output row
   __shared__ int warp_n[kMergeWarps], warp_g[kMergeWarps];
@@ -809,21 +822,22 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Tree
       return ex2(m2 - ref);
     };
     const int step = many ? 4 : 1;
+    const float* mine = p.part_o + ((lane & 7) >> 1) * kPartStep + 4 * (lane & 1);  // of a row
 #pragma unroll 1
-    for (int k = many ? lane >> 3 : 0; real && k < parts; k += 2 * step) {
-      float2 ml[2];
-      float4 x[2][V];
+    for (int k = many ? lane >> 3 : 0; real && k < parts; k += 4 * step) {
+      float2 ml[4];
+      float4 x[4][V];
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int f = 0; f < 4; ++f) {
         if (k + f * step >= parts) break;
         const int64_t at = slot(k + f * step) + row;
         ml[f] = p.part_ml[at];
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          x[f][e] = reinterpret_cast<const float4*>(p.part_o + at * D)[8 * e + (lane & 7)];
+          x[f][e] = *reinterpret_cast<const float4*>(mine + part_at<D>(at) + 4 * e * kPartStep);
       }
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int f = 0; f < 4; ++f) {
         if (k + f * step >= parts) break;
         if (ml[f].y == 0.f) continue;  // a part with nothing in it, whose o holds anything
         const float w = down(ml[f].x);
@@ -885,7 +899,7 @@ cudaError_t launch(const TreeLaunch& l) {
   e = launch_dependent(kern, dim3((unsigned)l.p.ctas), dim3(kThreads), Plan<D>::smem(l.p.B),
                        l.stream, l.p, l.tmap_q, l.tmap_k, l.tmap_v);
   if (e != cudaSuccess) return e;
-  return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)(2 * l.p.ctas)),
+  return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)l.p.ctas),
                           dim3(kMergeThreads), 0, l.stream, l.p);
 }
 
