@@ -16,7 +16,8 @@ namespace pkv {
 
 constexpr int kTreeRows = 128, kTreeTok = 128;  // rows of a tile, tokens of a block
 constexpr int kTreeBlock = 2, kTreeSeg = 4;
-constexpr int kTreeMinShare = 4;  // a share is worth at least this much
+constexpr int kTreeMinShare = 2;  // a share is worth at least a block (10.7 us for one
+                                  // sequence of 708 tokens, 12.6 for two blocks)
 constexpr int kTreeMaxBatch = 3328, kTreeMaxCtas = 256;
 static_assert(kTreeMinShare >= kTreeBlock, "no share without a block inside a segment");
 
