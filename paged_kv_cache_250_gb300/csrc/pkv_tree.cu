@@ -742,7 +742,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // registers: two with 64, whose loads spilled, took ragged trees of 32 sequences from 83
 // to 87.5 us and one sequence of 32768 tokens from 36 to 42.
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeAt = 4, kMergeFew = 4;
+constexpr int kMergeAt = 4;
+// Whether a row's parts are spread over a warp: more than four of a segment with few
+// rows, whose warps would else be few, or more than eight (64 nodes behind 701 tokens,
+// 224 rows in 6 parts: 16.8 us with four for all, 15.7; 28 rows: 11.0 with eight, 10.7).
+__device__ __forceinline__ bool merge_many(int parts, int rows) {
+  return parts > (rows > 32 ? 8 : 4);
+}
 constexpr int kMergeShares = 768;  // room for the shares of both lines
 constexpr int kMaxCtas = kMergeShares / 3;
 
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) tree_merge_kernel(const Tree
       m = p.meta[2 * i];
       o = p.meta[2 * i + 1];
     }
-    const int mine = m.x == 0 ? 0 : m.x > kMergeFew ? m.y : (m.y + kMergeAt - 1) / kMergeAt;
+    const int mine = m.x == 0 ? 0 : merge_many(m.x, m.y) ? m.y : (m.y + kMergeAt - 1) / kMergeAt;
     int g = mine;  // groups up to this entry's
 #pragma unroll
     for (int o2 = 1; o2 < 32; o2 <<= 1) {
@@ -805,7 +811,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) tree_merge_kernel(const Tree
     auto slot = [&](int k) -> int64_t {
       return first + (k == 0 ? 2 * (int64_t)c + 1 : 2 * (int64_t)(c + k)) * per;
     };
-    const bool many = parts > kMergeFew;
+    const bool many = merge_many(parts, rows);
     const int row = many ? sub : sub * kMergeAt + (lane >> 3);
     const bool real = row < rows;
     // against a running maximum, so that m, l and o of a part are loaded together
