@@ -32,9 +32,9 @@
 // waited for one stream's buffer while the other's was free).  Two tiles are bound by
 // each stream's chain of softmax (2200 cycles per block) and products (2200): 263 us
 // for the same cache and 64 nodes, 1.0 PFLOP/s counted, 1.6 with the second product
-// of P; the tensor pipe is active 70 % of the cycles.  Short segments and small calls
+// of P; the tensor pipe is active 73 % of the cycles.  Short segments and small calls
 // are bound by latency: 64 sequences of 512 tokens 42 us, of 128 tokens 20, one of 708
-// tokens 12.6, of which 3 are the merge behind.  A launch fetches its code anew, so
+// tokens 10.7, of which 3 are the merge behind.  A launch fetches its code anew, so
 // short code counts: scores masked in tensor memory before the softmax, instead of a
 // second softmax with masks, and one copy of it for both lines took a cold launch of
 // the smallest call from 24 to 15 us.
