@@ -396,7 +396,8 @@ PKV_API pkv_status pkv_paged_tree_attention(
 
 /* Keep the accepted path of each tree: the K and V rows (and per-token scales)
  * of its nodes move up behind the sequence's past, in the path's order.
- *   q_start       as for pkv_paged_tree_attention: n_b nodes in the last n_b of
+ *   q_start       int32 [batch + 1], device, non-decreasing, from 0 or more: n_b =
+ *                 q_start[b + 1] - q_start[b] nodes in the last n_b of
  *                 context_lens[b] positions; P_b = context_lens[b] - n_b.
  *   path          device int32 [batch][max_path]: entry i of sequence b, i <
  *                 path_lens[b], is the node whose row goes to position P_b + i

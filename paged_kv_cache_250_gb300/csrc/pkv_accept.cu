@@ -20,7 +20,9 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_path_kernel(const Accep
   __shared__ int32_t src_row[kMaxPath], dst_row[kMaxPath];  // of the pool; -1: nothing moves
   griddep_wait_then_trigger();
   const int node = tid < p.max_path ? p.path[(int64_t)b * p.max_path + tid] : 0;
-  const int ctx = p.context_lens[b], n = p.q_start[b + 1] - p.q_start[b], len = p.path_lens[b];
+  const int ctx = p.context_lens[b], len = p.path_lens[b];
+  const int q0 = p.q_start[b], q1 = p.q_start[b + 1];
+  const int n = q0 < 0 || q1 < q0 ? -1 : q1 - q0;
   if (ctx < 0 || ctx > p.MBS * kPageSize || n < 0 || n > ctx || len < 0 || len > n ||
       len > p.max_path) {
     if (h == 0 && tid == 0) report_error(p.err_word, PKV_ERR_BOUNDS);

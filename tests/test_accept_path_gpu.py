@@ -104,6 +104,21 @@ def test_path_lengths_out_of_range(bad):
     assert new.item() == -5 and p.err.item() == pkv.PKV_ERR_BOUNDS
 
 
+@pytest.mark.parametrize("first,last", [(9, 4), (-4, 5), (-9, 0), (2 ** 31 - 1, -2 ** 31),
+                                        (2 ** 31 - 3, -2 ** 31 + 5)])
+def test_starts_that_run_backwards_or_from_below_zero(first, last):
+    """Also where the difference of the two, cut to 32 bits, is a count like another."""
+    p = Paged([40], 8, 2, 128, "bf16", 12)
+    want = expect(p, [9], [[]])
+    new = torch.full((1,), -5, dtype=torch.int32, device="cuda")
+    pkv.pkv_kv_accept_path(p.desc, p.kc, p.vc, p.tables, p.ctx,
+                           torch.tensor([first, last], dtype=torch.int32).cuda(),
+                           torch.tensor([[0, 3]], dtype=torch.int32).cuda(),
+                           torch.tensor([0], dtype=torch.int32).cuda(), new)
+    same(p, want)
+    assert new.item() == -5 and p.err.item() == pkv.PKV_ERR_BOUNDS
+
+
 def test_blocks_outside_the_pool():
     p = Paged([60], 8, 2, 128, "bf16", 9)
     nodes, path = [40], [[30, 39, 25]]     # the tree lies at 20 .. 59
