@@ -184,6 +184,15 @@ __device__ __forceinline__ float cap_score(float x, float z_of_x, float cap_log2
   return fmaf(rcp(1.f + ex2(x * z_of_x)), -2.f * cap_log2, cap_log2);
 }
 
+// Softmax weights meet V as pairs of 16-bit values, hi + lo.  Pairs of bf16 keep 16
+// bits of any weight; those of fp16 end at 2^-24, and a weight relative to the row's
+// largest score would be nothing below 2^-25: behind a first token that scores 17.4
+// nats above 32767 others, all they bring.  So under fp16 the running reference stays
+// kRefBelow under the largest score, in log2 units.  Scores may outgrow it by 2^8 before
+// the next rescale: weights reach 2^15, and fp16 65504.
+template <bool IsBF16>
+constexpr float kRefBelow = IsBF16 ? 0.f : 7.f;
+
 // Two fp32 -> packed 16-bit pair (lo in the low half), round to nearest even.
 template <bool IsBF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {

@@ -25,7 +25,8 @@
 //   other's softmax.
 //   S = Q K^T   tcgen05.mma M 128 x N 128 x K d from shared memory;
 //   P           hi + lo 16-bit pairs over S in tensor memory (the weights keep
-//               about 16 bits, as in the framework's other attention kernels);
+//               about 16 bits; those of fp16 are off by up to 2^-32 of the row's
+//               largest besides: see kRefBelow);
 //   O += P V    tcgen05.mma with A from tensor memory, twice per 16 tokens.
 // One tile is bound by HBM: 8 x 32768 tokens of 8 KV heads and 8 nodes, 1.07 GB, 180
 // us, 6.0 TB/s (235 us while one warp copied K and V of both streams in turn: it
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           smax(sa);
           float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), its;
           ok = exchange(mx, ok, its);
-          mx = fmaxf(mx, its) * c2;
+          mx = fmaxf(mx, its) * c2 - kRefBelow<BF16>;
           const bool grow = mx > m_ref + 8.f;  // lazy rescale, as in the prefill kernel
           float alpha = 1.f;
           if (grow) {

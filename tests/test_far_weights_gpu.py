@@ -1,0 +1,128 @@
+"""Softmax weights far below the largest: a first token that takes nearly all the
+weight and whose V is zero (an attention sink) in front of thousands of tokens that
+weigh something only together.  What each of them weighs has to survive its rounding
+to the 16-bit pair that the tensor cores multiply with V."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_250_gb300 as pkv
+from ops_harness import CODE, DT, PAGE
+
+pytestmark = pytest.mark.gpu
+
+GAPS = (9.0, 14.0, 16.5, 17.4)  # nats between the first token's score and the others'
+
+
+class Sink:
+    """`batch` sequences of n tokens in the same blocks.  The token at `first` has a
+    key of 8 in element 0 and no value; the others have no key and values around 1."""
+
+    def __init__(self, n, batch, Hq, Hkv, d, cache, seed, first=0):
+        g = torch.Generator().manual_seed(seed)
+        self.n, self.batch, self.Hq, self.Hkv, self.d, self.first = n, batch, Hq, Hkv, d, first
+        self.fp8 = cache.startswith("e4m3")
+        pages = -(-n // PAGE)
+        self.NB = pages + 2
+        tables = torch.randperm(self.NB, generator=g)[:pages].to(torch.int32)
+        blk, off = tables.long().repeat_interleave(PAGE)[:n], torch.arange(n) % PAGE
+        v = 0.5 + torch.rand(n, Hkv, d, generator=g)
+        v[first] = 0.0
+        shape = (self.NB, Hkv, PAGE, d)
+        ks = vs = None
+        if self.fp8:  # codes of 256 v, scales of 1 / 256; the key a code of 256 under 1 / 32
+            kc, vc = torch.zeros(shape, dtype=torch.uint8), torch.zeros(shape, dtype=torch.uint8)
+            code = (v * 256).to(torch.float8_e4m3fn)
+            vc[blk, :, off] = code.view(torch.uint8)
+            self.V = code.double() / 256
+            kc[blk[first], :, off[first], 0] = torch.tensor([256.0]).to(
+                torch.float8_e4m3fn).view(torch.uint8)
+            if cache == "e4m3":
+                ks, vs = torch.full((Hkv,), 1 / 32), torch.full((Hkv,), 1 / 256)
+            else:
+                ks = torch.full((self.NB, Hkv, 2, PAGE), 1 / 256)
+                ks[:, :, 0] = 1 / 32
+        else:
+            kc, vc = torch.zeros(shape, dtype=DT[cache]), torch.zeros(shape, dtype=DT[cache])
+            v = v.to(DT[cache])
+            vc[blk, :, off] = v
+            self.V = v.double()
+            kc[blk[first], :, off[first], 0] = 8.0
+        self.qdt = DT.get(cache, torch.bfloat16)
+        self.scale = 1 / math.sqrt(d)
+        self.kc, self.vc = kc.cuda(), vc.cuda()
+        self.ks, self.vs = (None if t is None else t.cuda() for t in (ks, vs))
+        self.tables = tables.repeat(batch, 1).contiguous().cuda()
+        self.blocks = tables.cuda()
+        self.ctx = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.desc = pkv.make_desc(self.NB, PAGE, Hkv, Hq, d, CODE[cache], self.ks, self.vs,
+                                  self.err)
+
+    def queries(self, rows, seed):
+        """[rows][Hq][d]; the gaps in turn, row by row and head by head."""
+        g = torch.Generator().manual_seed(seed)
+        q = torch.randn(rows, self.Hq, self.d, generator=g)
+        at = torch.arange(rows)[:, None] + torch.arange(self.Hq)[None, :]
+        q[:, :, 0] = torch.tensor(GAPS)[at % len(GAPS)] / (8 * self.scale)
+        return q.to(self.qdt)
+
+    def check(self, out, q, seen, cap=0.0, slopes=None):
+        """out, q: [rows][Hq][d]; row r sees the first seen[r] tokens.
+
+        Off by, relative to the output: 2^-15 (pairs of bf16, exponentials, scores of
+        up to 26 in log2 units), 2^-21 of a cap; n 2^-24 for sums of n terms in fp32,
+        each cut at 2^-23 of the sum and 16 of them or more added at once.  And what
+        the pairs cannot hold: half a step of an fp16 subnormal, 2^-25, of n weights
+        that are kept 2^7 above their ratio to the largest."""
+        ref = {}
+        worst = 0.0
+        for r in range(out.shape[0]):
+            for h in range(self.Hq):
+                x = float(q[r, h, 0])
+                slope = 0.0 if slopes is None else float(slopes[h])
+                kv = h // (self.Hq // self.Hkv)
+                key = (x, slope, kv, seen[r])
+                if key not in ref:
+                    s = torch.zeros(seen[r], dtype=torch.float64)
+                    s[self.first] = x * 8 * self.scale
+                    if cap:
+                        s = cap * torch.tanh(s / cap)
+                    s += slope * (torch.arange(seen[r]).double() - (seen[r] - 1))
+                    ref[key] = torch.softmax(s, 0) @ self.V[:seen[r], kv]
+                want, n = ref[key], seen[r]
+                tol = want.abs() * (2.0 ** -15 + cap * 2.0 ** -21 + n * 2.0 ** -24) + \
+                    n * 2.0 ** -32 * 1.5
+                off = (out[r, h] - want).abs()
+                worst = max(worst, (off / tol).max().item())
+        assert worst <= 1.0, f"{worst:.3g} of the bound"
+        assert self.err.item() == 0
+
+
+def zeros(n):
+    return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+
+# As many sequences as leave each of them whole, or nearly, to one share of the work.
+@pytest.mark.parametrize("Hq,d,cache", [(1, 128, "f16"), (8, 64, "f16"), (4, 128, "bf16")])
+@pytest.mark.parametrize("nodes", [1, 40])
+def test_tree(Hq, d, cache, nodes):
+    s = Sink(32768, 320, Hq, 1, d, cache, 11)
+    q = s.queries(nodes, 12)
+    total = 320 * nodes
+    words = torch.tensor([1 << j for j in range(nodes)]).repeat(320).cuda()
+    out = torch.empty(total, Hq, d, device="cuda")
+    starts = (nodes * torch.arange(321)).int().cuda()
+    pkv.pkv_paged_tree_attention(s.desc, q.repeat(320, 1, 1).cuda(), s.kc, s.vc, s.tables, s.ctx,
+                                 starts, nodes, words, s.scale, out,
+                                 zeros(pkv.pkv_tree_workspace_bytes(s.desc, 320, nodes, 2048)))
+    out = out.view(320, nodes, Hq, d).double().cpu()
+    # a node sees the past and itself: as if it came right behind the past
+    see = [s.n - nodes + 1] * nodes
+    V = s.V
+    for b in (0, 1, 77, 200, 319):
+        for j in range(0, nodes, 13):
+            s.V = torch.cat([V[:s.n - nodes], V[s.n - nodes + j][None]])
+            s.check(out[b, j:j + 1], q[j:j + 1], see[:1])
+    s.V = V
