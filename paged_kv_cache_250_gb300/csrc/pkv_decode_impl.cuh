@@ -530,6 +530,9 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   float c2a = 0.f, c2b = 0.f;
   float sla = 0.f, slb = 0.f;  // biased: the same two columns' slopes, log2 units
   float* seg_scores = nullptr;  // scored: the scores of the current segment
+  // per-token E4M3: the unit, and the rescale threshold less its logarithm (scores are
+  // compared with a reference that holds it)
+  [[maybe_unused]] float v_unit = kLeastUnit, v_thr = 0.f;
 
   auto reset_state = [&]() {
 #pragma unroll
@@ -538,6 +541,8 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       for (int e = 0; e < 4; ++e) o[mt][e] = 0.f;
     m2[0] = m2[1] = -INFINITY;
     l2[0] = l2[1] = 0.f;
+    v_unit = kLeastUnit;
+    v_thr = kRescaleThreshold - log2_of_unit(kLeastUnit);
   };
 
   // row of q / out for MMA column c of segment (b, h): query token c / G,
@@ -792,9 +797,26 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
     }
-    const bool grow = (mx0 > m2[0] + kRescaleThreshold) || (mx1 > m2[1] + kRescaleThreshold);
+    const float thr = kTok ? v_thr : kRescaleThreshold;
+    bool grow = (mx0 > m2[0] + thr) || (mx1 > m2[1] + thr);
+    if constexpr (kTok) {  // (four compares: their maximum first took 202.7 us for 201.0)
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        grow |= (fabsf(vsc[i][0]) > v_unit) | (fabsf(vsc[i][1]) > v_unit);
+    }
     if (__any_sync(0xffffffffu, grow)) {
-      const float n0 = fmaxf(m2[0], mx0), n1 = fmaxf(m2[1], mx1);
+      float was = 0.f, is = 0.f;  // the unit's part of the reference
+      if constexpr (kTok) {
+        float top = 0.f;  // the largest V scale
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          top = fmaxf(top, fmaxf(fabsf(vsc[i][0]), fabsf(vsc[i][1])));
+        was = kRescaleThreshold - v_thr;
+        v_unit = fmaxf(v_unit, unit_above(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+        is = log2_of_unit(v_unit);
+        v_thr = kRescaleThreshold - is;
+      }
+      const float n0 = fmaxf(m2[0] - was, mx0) + is, n1 = fmaxf(m2[1] - was, mx1) + is;
       float a0 = exp2f(m2[0] - n0), a1 = exp2f(m2[1] - n1);
       if constexpr (QC > 1) {  // a column that has seen nothing yet stays as it is
         if (n0 == -INFINITY) a0 = 1.f;

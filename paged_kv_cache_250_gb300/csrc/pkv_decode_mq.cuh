@@ -511,6 +511,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
   // score scale in log2 units (E4M3: times the K scale) for the lane's two
   // C-fragment columns 2 c4 and 2 c4 + 1 of each group
   float c2a[CW], c2b[CW];
+  // per-token E4M3: the unit, and the rescale threshold less its logarithm (scores are
+  // compared with a reference that holds it)
+  [[maybe_unused]] float v_unit = kLeastUnit, v_thr = 0.f;
 
   auto reset_state = [&]() {
 #pragma unroll
@@ -522,6 +525,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
       m2[cg][0] = m2[cg][1] = -INFINITY;
       l2[cg][0] = l2[cg][1] = 0.f;
     }
+    v_unit = kLeastUnit;
+    v_thr = kRescaleThreshold - log2_of_unit(kLeastUnit);
   };
 
   // row of q / out for column c of segment (b, h): query token c / G,
@@ -776,6 +781,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
         mx[cg][1] = fmaxf(mx[cg][1], fmaxf(xx[1], xx[3]));
       }
     }
+    const float thr = kTok ? v_thr : kRescaleThreshold;
     bool grow = false;
 #pragma unroll
     for (int cg = 0; cg < CW; ++cg) {
@@ -784,13 +790,27 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
         mx[cg][0] = fmaxf(mx[cg][0], __shfl_xor_sync(0xffffffffu, mx[cg][0], off));
         mx[cg][1] = fmaxf(mx[cg][1], __shfl_xor_sync(0xffffffffu, mx[cg][1], off));
       }
-      grow = grow || (mx[cg][0] > m2[cg][0] + kRescaleThreshold) ||
-             (mx[cg][1] > m2[cg][1] + kRescaleThreshold);
+      grow = grow || (mx[cg][0] > m2[cg][0] + thr) || (mx[cg][1] > m2[cg][1] + thr);
+    }
+    [[maybe_unused]] float v_top = 0.f;  // the largest V scale in the lane's rows
+    if constexpr (kTok) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        v_top = fmaxf(v_top, fmaxf(fabsf(vsc[i][0]), fabsf(vsc[i][1])));
+      grow = grow || v_top > v_unit;
     }
     if (__any_sync(0xffffffffu, grow)) {
+      float was = 0.f, is = 0.f;  // the unit's part of the reference
+      if constexpr (kTok) {
+        was = kRescaleThreshold - v_thr;
+        v_unit = fmaxf(v_unit, unit_above(__reduce_max_sync(0xffffffffu, __float_as_uint(v_top))));
+        is = log2_of_unit(v_unit);
+        v_thr = kRescaleThreshold - is;
+      }
 #pragma unroll
       for (int cg = 0; cg < CW; ++cg) {
-        const float n0 = fmaxf(m2[cg][0], mx[cg][0]), n1 = fmaxf(m2[cg][1], mx[cg][1]);
+        const float n0 = fmaxf(m2[cg][0] - was, mx[cg][0]) + is;
+        const float n1 = fmaxf(m2[cg][1] - was, mx[cg][1]) + is;
         float a0 = exp2f(m2[cg][0] - n0), a1 = exp2f(m2[cg][1] - n1);
         if constexpr (QC > 1) {  // a column that has seen nothing yet stays as it is
           if (n0 == -INFINITY) a0 = 1.f;

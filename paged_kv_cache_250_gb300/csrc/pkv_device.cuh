@@ -193,6 +193,23 @@ __device__ __forceinline__ float cap_score(float x, float z_of_x, float cap_log2
 template <bool IsBF16>
 constexpr float kRefBelow = IsBF16 ? 0.f : 7.f;
 
+// Per-token E4M3: a row's V scale goes into its weight, and the pair of fp16 values
+// needs their product in fp16's range whatever size V is.  So weights are relative to a
+// reference that holds, beside the largest score, a power of two (the unit) that no V
+// scale seen so far exceeds: it starts at the least one, and a larger scale moves it up
+// as a larger score does.  l and o share the reference as ever.  (Without it V rows of
+// 2^-10 came out 0.5 % off, and rows above 2^17 as infinities.)  Units span 2^124, so that
+// a step from the least to the most still leaves of l, in fp32, what weighs more than
+// 2^-25 of the rest.  64 x 8192 tokens take 201.0 us as before; with o in units of its
+// own and the scales divided by them 204.0.
+constexpr float kLeastUnit = 0x1p-40f, kMostUnit = 0x1p84f;
+__device__ __forceinline__ float unit_above(uint32_t top) {  // top: a float >= 0, its bits
+  return fminf(fmaxf(__uint_as_float(((top >> 23) + 1) << 23), kLeastUnit), kMostUnit);
+}
+__device__ __forceinline__ float log2_of_unit(float unit) {
+  return (float)((int)(__float_as_uint(unit) >> 23) - 127);
+}
+
 // Two fp32 -> packed 16-bit pair (lo in the low half), round to nearest even.
 template <bool IsBF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
