@@ -46,13 +46,15 @@
 //                                           page, Q^T resident in registers;
 //                                           the 8 columns are the g query
 //                                           heads of the group (zero-padded)
-//   online softmax in registers (log2 domain); the running max only moves
-//   when a tile's max exceeds it by more than 2^8, which keeps every weight
-//   p <= 256 and is exact because l and o use the same reference;
+//   online softmax in registers (log2 domain); the reference only moves when
+//   a tile's max exceeds it by more than 2^8, which keeps every weight
+//   p <= 2^8 (fp16 operands, whose reference lies 2^7 below the maximum it
+//   was taken from: 2^15) and is exact because l and o use the same one;
 //   O^T[d][8] += V^T[d][16] . P^T[16][8]    V^T via ldmatrix.trans, P^T via
 //                                           movmatrix; P is split into hi + lo
 //                                           16-bit parts (two MMAs) so the
-//                                           weights keep ~16 mantissa bits.
+//                                           weights keep ~16 mantissa bits
+//                                           (fp16: see kRefBelow).
 // E4M3 pages are converted to fp16 in registers (exact) after the ldmatrix;
 // the per-head K scale is folded into the score scale and the V scale into
 // the output.
@@ -530,9 +532,11 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
   float c2a = 0.f, c2b = 0.f;
   float sla = 0.f, slb = 0.f;  // biased: the same two columns' slopes, log2 units
   float* seg_scores = nullptr;  // scored: the scores of the current segment
-  // per-token E4M3: the unit, and the rescale threshold less its logarithm (scores are
-  // compared with a reference that holds it)
-  [[maybe_unused]] float v_unit = kLeastUnit, v_thr = 0.f;
+  // fp16 operands: how far the segment's reference lies below the maximum it was taken
+  // from.  per-token E4M3: the unit, whose logarithm the reference holds.  thr: what a
+  // score may be above the reference.
+  [[maybe_unused]] float below = 0.f, v_unit = kLeastUnit;
+  float thr = kRescaleThreshold;
 
   auto reset_state = [&]() {
 #pragma unroll
@@ -542,7 +546,6 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
     m2[0] = m2[1] = -INFINITY;
     l2[0] = l2[1] = 0.f;
     v_unit = kLeastUnit;
-    v_thr = kRescaleThreshold - log2_of_unit(kLeastUnit);
   };
 
   // row of q / out for MMA column c of segment (b, h): query token c / G,
@@ -797,7 +800,6 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
     }
-    const float thr = kTok ? v_thr : kRescaleThreshold;
     bool grow = (mx0 > m2[0] + thr) || (mx1 > m2[1] + thr);
     if constexpr (kTok) {  // (four compares: their maximum first took 202.7 us for 201.0)
 #pragma unroll
@@ -811,12 +813,13 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
 #pragma unroll
         for (int i = 0; i < NP; ++i)
           top = fmaxf(top, fmaxf(fabsf(vsc[i][0]), fabsf(vsc[i][1])));
-        was = kRescaleThreshold - v_thr;
+        was = kRescaleThreshold + below - thr;
         v_unit = fmaxf(v_unit, unit_above(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
         is = log2_of_unit(v_unit);
-        v_thr = kRescaleThreshold - is;
+        thr = kRescaleThreshold + below - is;
       }
-      const float n0 = fmaxf(m2[0] - was, mx0) + is, n1 = fmaxf(m2[1] - was, mx1) + is;
+      const float n0 = fmaxf(m2[0] - was, mx0 - below) + is;
+      const float n1 = fmaxf(m2[1] - was, mx1 - below) + is;
       float a0 = exp2f(m2[0] - n0), a1 = exp2f(m2[1] - n1);
       if constexpr (QC > 1) {  // a column that has seen nothing yet stays as it is
         if (n0 == -INFINITY) a0 = 1.f;
@@ -1259,6 +1262,9 @@ __global__ void __launch_bounds__(decode_warps((CacheKind)CACHE) * 32, kDecodeCt
         pages_mine = 0;
         have_q = false;
         reset_state();
+        if constexpr (!kBF) below = ref_below(np);
+        thr = kRescaleThreshold + below;
+        if constexpr (kTok) thr -= log2_of_unit(kLeastUnit);
         if constexpr (kScored)
           seg_scores = p.scores + ((int64_t)b * p.Hkv + h) * p.MBS * (kPageSize * G);
         split = x > seg_start || seg_end > sh_hi;

@@ -192,6 +192,12 @@ __device__ __forceinline__ float cap_score(float x, float z_of_x, float cap_log2
 // the next rescale: weights reach 2^15, and fp16 65504.
 template <bool IsBF16>
 constexpr float kRefBelow = IsBF16 ? 0.f : 7.f;
+// The decode kernels leave it out under up to 16 pages, whose weights lose 2^-17 of the
+// largest together, less than the pairs' own roundings: there the largest weighs exactly
+// 1, and a sequence of one token gives its V row as it is.
+__device__ __forceinline__ float ref_below(int pages) {
+  return pages > 16 ? kRefBelow<false> : 0.f;
+}
 
 // Per-token E4M3: a row's V scale goes into its weight, and the pair of fp16 values
 // needs their product in fp16's range whatever size V is.  So weights are relative to a

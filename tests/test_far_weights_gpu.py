@@ -126,3 +126,36 @@ def test_tree(Hq, d, cache, nodes):
             s.V = torch.cat([V[:s.n - nodes], V[s.n - nodes + j][None]])
             s.check(out[b, j:j + 1], q[j:j + 1], see[:1])
     s.V = V
+
+
+def decode_out(s, q, call, **kw):
+    out = torch.empty(q.shape, device="cuda")
+    call(s.desc, q.cuda(), s.kc, s.vc, s.tables, s.ctx, out=out, scale=s.scale, **kw)
+    return out.double().cpu()
+
+
+CACHES = [("f16", 128, 1), ("f16", 64, 8), ("bf16", 128, 4), ("e4m3", 128, 4), ("e4m3tok", 128, 4),
+          ("e4m3tok", 128, 1)]
+
+
+@pytest.mark.parametrize("cache,d,Hq", CACHES)
+@pytest.mark.parametrize("batch", [1, 320])
+@pytest.mark.parametrize("form", ["plain", "scored", "cap", "distance"])
+def test_decode(cache, d, Hq, batch, form):
+    s = Sink(32768, batch, Hq, 1, d, cache, 21)
+    q = s.queries(batch, 22)
+    ws = zeros(pkv.pkv_decode_workspace_bytes(s.desc, batch, 2048))
+    cap, slopes = 0.0, None
+    if form == "plain":
+        out = decode_out(s, q, pkv.pkv_paged_decode_attention, workspace=ws)
+    elif form == "scored":
+        ws = zeros(pkv.pkv_scored_workspace_bytes(s.desc, batch, 2048))
+        out = decode_out(s, q, pkv.pkv_paged_decode_attention_scored, workspace=ws, decay=0.0,
+                         weights=torch.zeros(s.NB, 1, PAGE, device="cuda"))
+    else:
+        cap = 50.0 if form == "cap" else 0.0
+        slopes = torch.full((Hq,), 2.0 ** -16) if form == "distance" else None
+        out = decode_out(s, q, pkv.pkv_paged_decode_attention_biased, workspace=ws, softcap=cap,
+                         alibi_slopes=None if slopes is None else slopes.cuda())
+    at = list(range(0, batch, 40))
+    s.check(out[at], q[at], [s.n] * len(at), cap, slopes)
