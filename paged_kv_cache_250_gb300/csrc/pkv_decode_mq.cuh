@@ -50,13 +50,15 @@
 //                                           page, Q^T resident in registers;
 //                                           the 8 columns are (query token,
 //                                           head) pairs (zero-padded)
-//   online softmax in registers (log2 domain); the running max only moves
-//   when a tile's max exceeds it by more than 2^8, which keeps every weight
-//   p <= 256 and is exact because l and o use the same reference;
+//   online softmax in registers (log2 domain); the reference only moves when
+//   a tile's max exceeds it by more than 2^8, which keeps every weight
+//   p <= 2^8 (fp16 operands, whose reference lies 2^7 below the maximum it
+//   was taken from: 2^15) and is exact because l and o use the same one;
 //   O^T[d][8] += V^T[d][16] . P^T[16][8]    V^T via ldmatrix.trans, P^T via
 //                                           movmatrix; P is split into hi + lo
 //                                           16-bit parts (two MMAs) so the
-//                                           weights keep ~16 mantissa bits.
+//                                           weights keep ~16 mantissa bits
+//                                           (fp16: see kRefBelow).
 // E4M3 pages are converted to fp16 in registers (exact) after the ldmatrix;
 // the per-head K scale is folded into the score scale and the V scale into
 // the output.
@@ -511,9 +513,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
   // score scale in log2 units (E4M3: times the K scale) for the lane's two
   // C-fragment columns 2 c4 and 2 c4 + 1 of each group
   float c2a[CW], c2b[CW];
-  // per-token E4M3: the unit, and the rescale threshold less its logarithm (scores are
-  // compared with a reference that holds it)
-  [[maybe_unused]] float v_unit = kLeastUnit, v_thr = 0.f;
+  // fp16 operands: how far the segment's reference lies below the maximum it was taken
+  // from.  per-token E4M3: the unit, whose logarithm the reference holds.  thr: what a
+  // score may be above the reference.
+  [[maybe_unused]] float below = 0.f, v_unit = kLeastUnit;
+  float thr = kRescaleThreshold;
 
   auto reset_state = [&]() {
 #pragma unroll
@@ -526,7 +530,6 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
       l2[cg][0] = l2[cg][1] = 0.f;
     }
     v_unit = kLeastUnit;
-    v_thr = kRescaleThreshold - log2_of_unit(kLeastUnit);
   };
 
   // row of q / out for column c of segment (b, h): query token c / G,
@@ -781,7 +784,6 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
         mx[cg][1] = fmaxf(mx[cg][1], fmaxf(xx[1], xx[3]));
       }
     }
-    const float thr = kTok ? v_thr : kRescaleThreshold;
     bool grow = false;
 #pragma unroll
     for (int cg = 0; cg < CW; ++cg) {
@@ -802,15 +804,15 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
     if (__any_sync(0xffffffffu, grow)) {
       float was = 0.f, is = 0.f;  // the unit's part of the reference
       if constexpr (kTok) {
-        was = kRescaleThreshold - v_thr;
+        was = kRescaleThreshold + below - thr;
         v_unit = fmaxf(v_unit, unit_above(__reduce_max_sync(0xffffffffu, __float_as_uint(v_top))));
         is = log2_of_unit(v_unit);
-        v_thr = kRescaleThreshold - is;
+        thr = kRescaleThreshold + below - is;
       }
 #pragma unroll
       for (int cg = 0; cg < CW; ++cg) {
-        const float n0 = fmaxf(m2[cg][0] - was, mx[cg][0]) + is;
-        const float n1 = fmaxf(m2[cg][1] - was, mx[cg][1]) + is;
+        const float n0 = fmaxf(m2[cg][0] - was, mx[cg][0] - below) + is;
+        const float n1 = fmaxf(m2[cg][1] - was, mx[cg][1] - below) + is;
         float a0 = exp2f(m2[cg][0] - n0), a1 = exp2f(m2[cg][1] - n1);
         if constexpr (QC > 1) {  // a column that has seen nothing yet stays as it is
           if (n0 == -INFINITY) a0 = 1.f;
@@ -1234,6 +1236,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm)
     while (nfl < s) flush_next();
     if (cur != s) {
       cur = s;
+      if constexpr (!kBF) below = ref_below(pfx[b + 1] - pfx[b]);
+      thr = kRescaleThreshold + below;
+      if constexpr (kTok) thr -= log2_of_unit(kLeastUnit);
       load_q(b, h);
     }
   };

@@ -159,3 +159,15 @@ def test_decode(cache, d, Hq, batch, form):
                          alibi_slopes=None if slopes is None else slopes.cuda())
     at = list(range(0, batch, 40))
     s.check(out[at], q[at], [s.n] * len(at), cap, slopes)
+
+
+@pytest.mark.parametrize("cache,d,Hq", CACHES)
+@pytest.mark.parametrize("batch", [1, 320])
+@pytest.mark.parametrize("q_len", [2, 8])
+def test_multi_query(cache, d, Hq, batch, q_len):
+    s = Sink(32768, batch, Hq, 1, d, cache, 31)
+    q = s.queries(batch * q_len, 32).view(batch, q_len, Hq, d)
+    ws = zeros(pkv.pkv_decode_workspace_bytes_multi(s.desc, batch, q_len, 2048))
+    out = decode_out(s, q, pkv.pkv_paged_decode_attention_multi, workspace=ws)
+    for b in range(0, batch, 80):
+        s.check(out[b], q[b], [s.n - q_len + j + 1 for j in range(q_len)])
