@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       };
       if (full) max_pass(Masked<false>{});
       else max_pass(Masked<true>{});
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+      const float mx =
+          fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2 - kRefBelow<BF16>;
       // lazy rescale: keep the reference max while scores stay within 2^8 of it
       const bool grow = mx > m_ref + 8.f;
       float alpha = 1.f;

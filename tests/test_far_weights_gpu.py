@@ -171,3 +171,21 @@ def test_multi_query(cache, d, Hq, batch, q_len):
     out = decode_out(s, q, pkv.pkv_paged_decode_attention_multi, workspace=ws)
     for b in range(0, batch, 80):
         s.check(out[b], q[b], [s.n - q_len + j + 1 for j in range(q_len)])
+
+
+@pytest.mark.parametrize("cache,d,Hq", CACHES[:3])
+@pytest.mark.parametrize("form", ["plain"])
+def test_prefill(cache, d, Hq, form):
+    rows = 40
+    s = Sink(32768, 1, Hq, 1, d, cache, 51)
+    q = s.queries(rows, 52)
+    starts = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    kw, cap, slopes = {}, 0.0, None
+    call = pkv.pkv_paged_prefill_attention
+    if form != "plain":
+        call = pkv.pkv_paged_prefill_attention_biased
+        cap = 50.0 if form != "distance" else 0.0
+        slopes = torch.full((Hq,), 2.0 ** -16) if form != "cap" else None
+        kw = dict(softcap=cap, alibi_slopes=None if slopes is None else slopes.cuda())
+    out = decode_out(s, q, call, q_start=starts, max_q_len=rows, **kw)
+    s.check(out[::13], q[::13], [s.n - rows + j + 1 for j in range(0, rows, 13)], cap, slopes)
