@@ -327,6 +327,7 @@ __device__ __forceinline__ bool softmax_steps(const Cta& c, int N, int t, int tt
     if constexpr (!kDist) {  // a cap alone keeps the order of the scores: the largest alone
       if (mx > -INFINITY) mx = f2_split(cap_pair(f2(mx, mx), cap2)).x;
     }
+    mx -= kRefBelow<BF16>;
     // lazy rescale: keep the reference max while scores stay within 2^8 of it
     const bool grow = mx > m_ref + 8.f;
     float alpha = 1.f;

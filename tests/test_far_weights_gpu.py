@@ -174,7 +174,7 @@ def test_multi_query(cache, d, Hq, batch, q_len):
 
 
 @pytest.mark.parametrize("cache,d,Hq", CACHES[:3])
-@pytest.mark.parametrize("form", ["plain"])
+@pytest.mark.parametrize("form", ["plain", "cap", "distance", "both"])
 def test_prefill(cache, d, Hq, form):
     rows = 40
     s = Sink(32768, 1, Hq, 1, d, cache, 51)
