@@ -23,7 +23,8 @@
 // softmax.
 //   S = Q K^T   tcgen05.mma M 128 x N 128 x K d from shared memory;
 //   P           hi + lo 16-bit pairs over S in tensor memory (the weights keep
-//               about 16 bits, as in the framework's other attention kernels);
+//               about 16 bits; those of fp16 are off by up to 2^-32 of the row's
+//               largest besides: see kRefBelow);
 //   O += P V    tcgen05.mma with A from tensor memory, twice per 16 tokens.
 // Bound by the softmax and the products taking turns on each stream.  256
 // sequences behind 32768 tokens, 32/8 heads of 128: 8192 units in 149 us, 0.92
@@ -431,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (full) max_pass(Masked<false>{});
       else max_pass(Masked<true>{});
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+      const float mx =
+          fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2 - kRefBelow<BF16>;
       const bool grow = mx > m_ref + 8.f;  // lazy rescale, as in the prefill kernel
       float alpha = 1.f;
       if (grow) {
@@ -712,8 +714,9 @@ __global__ void __launch_bounds__(32)
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
     }
-    if (__any_sync(0xffffffffu, mx0 > m2[0] + 8.f || mx1 > m2[1] + 8.f)) {  // lazy rescale
-      const float n0 = fmaxf(m2[0], mx0), n1 = fmaxf(m2[1], mx1);
+    constexpr float kBelow = kRefBelow<BF16>, kGrowth = 8.f + kBelow;
+    if (__any_sync(0xffffffffu, mx0 > m2[0] + kGrowth || mx1 > m2[1] + kGrowth)) {  // lazy rescale
+      const float n0 = fmaxf(m2[0], mx0 - kBelow), n1 = fmaxf(m2[1], mx1 - kBelow);
       const float a0 = n0 == -INFINITY ? 1.f : ex2(m2[0] - n0);
       const float a1 = n1 == -INFINITY ? 1.f : ex2(m2[1] - n1);
       m2[0] = n0;

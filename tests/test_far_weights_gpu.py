@@ -189,3 +189,20 @@ def test_prefill(cache, d, Hq, form):
         kw = dict(softcap=cap, alibi_slopes=None if slopes is None else slopes.cuda())
     out = decode_out(s, q, call, q_start=starts, max_q_len=rows, **kw)
     s.check(out[::13], q[::13], [s.n - rows + j + 1 for j in range(0, rows, 13)], cap, slopes)
+
+
+# The first token in the shared prefix, with and without a pass of its own for that
+# (320 sequences and 2), and in what is each sequence's own (prefix of one block).
+@pytest.mark.parametrize("cache,d,Hq", CACHES[:3])
+@pytest.mark.parametrize("batch,prefix,first", [(320, 30000, 0), (2, 30000, 0), (320, 16, 16)])
+def test_shared_prefix(cache, d, Hq, batch, prefix, first):
+    s = Sink(32768, batch, Hq, 1, d, cache, 41, first)
+    q = s.queries(batch, 42)
+    npb = prefix // PAGE
+    ws = zeros(pkv.pkv_shared_prefix_workspace_bytes(s.desc, batch, npb, 2048))
+    out = torch.empty(q.shape, device="cuda")
+    pkv.pkv_paged_decode_attention_shared_prefix(s.desc, q.cuda(), s.kc, s.vc,
+                                                 s.blocks[:npb].contiguous(), s.tables, s.ctx,
+                                                 s.scale, out, ws)
+    at = list(range(0, batch, 40))
+    s.check(out.double().cpu()[at], q[at], [s.n] * len(at))
