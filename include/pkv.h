@@ -329,8 +329,12 @@ PKV_API size_t pkv_scored_workspace_bytes(const pkv_cache_desc* desc, int32_t ba
  * on position u, the weight of u under KV head h becomes
  *   w[u] = decay w[u] + sum of p_hq[u] over the query heads hq of h
  * (fp32).  The newest position's weight (context_lens[b] - 1) is set to its
- * sum, so a row need not be cleared when it is appended; with decay 0 every
- * position's is, whatever was there (the first call after a prompt).
+ * sum, so a row that comes with this step need not be cleared; with decay 0
+ * every position's is, whatever was there (the first call after a prompt).  Rows
+ * that came otherwise since the sequence's last scored call, several at a time
+ * (a chunk of a prompt, drafts and the path accepted of them) or in steps of
+ * another call, weigh what their slots held before until the caller sets their
+ * weights (to 0), before this call adds to them; a NaN would stay.
  *   weights       device fp32 [num_blocks][num_kv_heads][page_size], beside the
  *                 caches: the weight of the row in the same block and slot;
  *                 16-byte aligned.  Entries of positions the call does not see stay as they are.
@@ -407,12 +411,14 @@ PKV_API pkv_status pkv_paged_tree_attention(
  *   path_lens     device int32 [batch], 0 .. min(n_b, max_path).
  *   new_context_lens  device int32 [batch] or NULL: P_b + path_lens[b].  Must
  *                 not overlap the other arrays of the call.
- * Rows behind the new length keep what they held.  A sequence whose lengths
- * break the rules is a device-detected PKV_ERR_BOUNDS and stays as it is, its
- * entry of new_context_lens too; a node or block out of range is PKV_ERR_BOUNDS
- * and that step's row is not moved.  Blocks that receive a row must belong to
- * one sequence of the call (copy shared ones first: pkv_copy_blocks).  All cache
- * types. */
+ * Rows behind the new length keep what they held.  Weights and positions (see
+ * pkv_kv_evict) do not move with the rows: where both are in use, set the
+ * accepted rows' weights before the next pkv_paged_decode_attention_scored.  A
+ * sequence whose lengths break the rules is a device-detected PKV_ERR_BOUNDS and
+ * stays as it is, its entry of new_context_lens too; a node or block out of range
+ * is PKV_ERR_BOUNDS and that step's row is not moved.  Blocks that receive a row
+ * must belong to one sequence of the call (copy shared ones first:
+ * pkv_copy_blocks).  All cache types. */
 PKV_API pkv_status pkv_kv_accept_path(
     const pkv_cache_desc* desc, void* k_cache, void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens,
@@ -430,7 +436,8 @@ PKV_API pkv_status pkv_kv_accept_path(
  * position).  So a cache's rows lose their order (attention does not see it:
  * keys are rotated when they are appended), and `positions` says which token a
  * row belongs to.  A sequence of at most `budget` rows keeps them all.
- *   weights       as for pkv_paged_decode_attention_scored.
+ *   weights       as for pkv_paged_decode_attention_scored; those of all n rows
+ *                 count, so rows that no scored call has seen need one too.
  *   positions     device int32 [num_blocks][num_kv_heads][page_size]: the token
  *                 (0, 1, ...) of the row in the same block and slot; 16-byte
  *                 aligned.

@@ -530,7 +530,8 @@ def pkv_paged_decode_attention_scored(desc: CacheDesc, q: torch.Tensor, k_cache:
                                       stream=None) -> None:
     """As pkv_paged_decode_attention; weights (fp32 [num_blocks][Hkv][16]) of the
     rows seen become decay * weights + the attention weight of the KV head's query
-    heads, the newest row's (and with decay 0 all of them) the latter alone."""
+    heads, the newest row's (and with decay 0 all of them) the latter alone.  Set the
+    weights of other rows that came since the last such call (to 0) before this one."""
     lib = _lib or load_library()
     dev = q.get_device()
     if not _is_current(dev):
@@ -641,7 +642,8 @@ def pkv_kv_accept_path(desc: CacheDesc, k_cache: torch.Tensor, v_cache: torch.Te
                        new_context_lens: Optional[torch.Tensor] = None, stream=None) -> None:
     """The rows of nodes path[b][:path_lens[b]] (int32 [B][max_path]) of each
     sequence's tree move up behind its past, in that order; new_context_lens (int32
-    [B], written) counts the past and the path."""
+    [B], written) counts the past and the path.  Weights and positions of rows (see
+    pkv_kv_evict) do not move."""
     lib = _lib or load_library()
     dev = k_cache.get_device()
     if not _is_current(dev):
