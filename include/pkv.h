@@ -456,9 +456,15 @@ PKV_API pkv_status pkv_kv_accept_path(
  * lengths break the rules is a device-detected PKV_ERR_BOUNDS and stays as it
  * is, its entry of new_context_lens too.  A table entry outside the pool is
  * PKV_ERR_BOUNDS: its rows are the first to go and are never read or written.
+ * Where such a page lies below the budget its places are among those that kept
+ * rows from behind move into, and a row whose place is there is lost, one of the
+ * first or most recent tokens' too, although new_context_lens counts it: after
+ * that error the sequence's cache is not whole.  Check tables before the call.
  * Blocks must belong to one sequence of the call (copy shared ones first:
- * pkv_copy_blocks).  Tables of up to 49152 blocks per sequence (more returns
- * PKV_ERR_UNSUPPORTED).  All cache types; no workspace. */
+ * pkv_copy_blocks, and their weights and positions, which it does not copy).
+ * Tables of up to 49152 blocks per sequence (more returns PKV_ERR_UNSUPPORTED);
+ * the launch is laid out for max_blocks_per_seq, so that a table no wider than
+ * the rows there can be is fastest.  All cache types; no workspace. */
 PKV_API pkv_status pkv_kv_evict(
     const pkv_cache_desc* desc, void* k_cache, void* v_cache, float* weights,
     int32_t* positions, const int32_t* block_tables,

@@ -12,7 +12,8 @@
 // Where.  Kept rows below the budget stay where they are.  The rows below it
 // that go are holes, and the i-th kept row behind the budget moves into the
 // i-th hole: no more rows move than have to, sources and destinations never
-// meet, and the order is the same on every run.
+// meet, and the order is the same on every run.  (A hole in a page outside the pool
+// takes no row: the one that was to move there is lost, and the error reported.)
 //
 // One cluster of CL CTAs per (sequence, KV head), each with a contiguous slice
 // of the rows: the keys stay in shared memory, a warp takes a contiguous stretch
