@@ -349,108 +349,108 @@ __global__ void __launch_bounds__(kThreads, 1)
     // blocks of each stream and uses of each buffer so far, segments so far
     uint32_t st = 0, u0 = 0, u1 = 0, segs = 0;
     bool ok = true;
-      constexpr uint32_t kIdS = idesc_f16(BF16, false, kRows, kTok);
-      constexpr uint32_t kIdO = idesc_f16(BF16, true, kRows, D);
-      auto commit = [&](int i) {
-        armed[i] = armed[i] + 1;
-        umma_commit(bar(i));
-      };
-      const uint64_t dq = sdesc(base, 16, 1024);
-      const uint64_t dk = sdesc(base + kOffK, 16, 1024);
-      const uint64_t dv = sdesc(base + kOffV, kHalf, 1024);
-      // Q's slot t; bb: the buffer; last: nothing uses the buffer after this; q_last:
-      // nothing uses the slot
-      auto qk = [&](int t, int bb, bool last, bool q_last) {
-        const uint64_t a0 = dq + (t ? (uint64_t)NH * kHalf >> 4 : 0ull);
-        const uint64_t b0 = dk + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
+    constexpr uint32_t kIdS = idesc_f16(BF16, false, kRows, kTok);
+    constexpr uint32_t kIdO = idesc_f16(BF16, true, kRows, D);
+    auto commit = [&](int i) {
+      armed[i] = armed[i] + 1;
+      umma_commit(bar(i));
+    };
+    const uint64_t dq = sdesc(base, 16, 1024);
+    const uint64_t dk = sdesc(base + kOffK, 16, 1024);
+    const uint64_t dv = sdesc(base + kOffV, kHalf, 1024);
+    // Q's slot t; bb: the buffer; last: nothing uses the buffer after this; q_last:
+    // nothing uses the slot
+    auto qk = [&](int t, int bb, bool last, bool q_last) {
+      const uint64_t a0 = dq + (t ? (uint64_t)NH * kHalf >> 4 : 0ull);
+      const uint64_t b0 = dk + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32;
-          umma(tmem + (uint32_t)t * kTok, a0 + (off >> 4), b0 + (off >> 4), kIdS, ks > 0);
-        }
-        commit(kBarSFull + t);
-        if (last) commit(kBarKFree + bb);
-        if (q_last) commit(kBarQFree + t);
-      };
-      // P_t: per 16 tokens eight columns of hi pairs, then eight of lo pairs
-      auto pv = [&](int t, int bb, bool add, bool last) {
-        const uint64_t b0 = dv + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
-        const uint32_t pt = tmem + (uint32_t)t * kTok;
-        const uint32_t dt = tmem + 256 + (uint32_t)t * D;
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = (uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32;
+        umma(tmem + (uint32_t)t * kTok, a0 + (off >> 4), b0 + (off >> 4), kIdS, ks > 0);
+      }
+      commit(kBarSFull + t);
+      if (last) commit(kBarKFree + bb);
+      if (q_last) commit(kBarQFree + t);
+    };
+    // P_t: per 16 tokens eight columns of hi pairs, then eight of lo pairs
+    auto pv = [&](int t, int bb, bool add, bool last) {
+      const uint64_t b0 = dv + (bb ? (uint64_t)NH * kHalf >> 4 : 0ull);
+      const uint32_t pt = tmem + (uint32_t)t * kTok;
+      const uint32_t dt = tmem + 256 + (uint32_t)t * D;
 #pragma unroll
-        for (int ks = 0; ks < kTok / 16; ++ks) {
-          const uint64_t bv = b0 + ((uint32_t)ks * 16 * 128 >> 4);
-          umma_ts(dt, pt + (uint32_t)ks * 16, bv, kIdO, add || ks > 0);
-          umma_ts(dt, pt + (uint32_t)ks * 16 + 8, bv, kIdO, 1);
-        }
-        commit(kBarODone + t);
-        if (last) commit(kBarVFree + bb);
-      };
-      // The first product over O_t of a part comes after P_t, which the softmax
-      // threads hand over after they have read the last part's O_t out.
-      if (elect_one()) {
-        begin(0);
-        while (ok && next()) {  // one buffer after the other, both streams from it
-          const int n = wk.s.nblk;
-          if (warp == kWarpMma) {  // (the other counts)
-            uint32_t a0 = u0, a1 = u1;  // uses of the next block's buffer
-            ok = wait(kBarKFull, a0 & 1) && wait(kBarQ, segs & 1) && wait(kBarQ + 1, segs & 1);
-            if (!ok) break;
+      for (int ks = 0; ks < kTok / 16; ++ks) {
+        const uint64_t bv = b0 + ((uint32_t)ks * 16 * 128 >> 4);
+        umma_ts(dt, pt + (uint32_t)ks * 16, bv, kIdO, add || ks > 0);
+        umma_ts(dt, pt + (uint32_t)ks * 16 + 8, bv, kIdO, 1);
+      }
+      commit(kBarODone + t);
+      if (last) commit(kBarVFree + bb);
+    };
+    // The first product over O_t of a part comes after P_t, which the softmax
+    // threads hand over after they have read the last part's O_t out.
+    if (elect_one()) {
+      begin(0);
+      while (ok && next()) {  // one buffer after the other, both streams from it
+        const int n = wk.s.nblk;
+        if (warp == kWarpMma) {  // (the other counts)
+          uint32_t a0 = u0, a1 = u1;  // uses of the next block's buffer
+          ok = wait(kBarKFull, a0 & 1) && wait(kBarQ, segs & 1) && wait(kBarQ + 1, segs & 1);
+          if (!ok) break;
+          tc_fence_after();
+          qk(0, 0, false, n == 1);
+          qk(1, 0, true, n == 1);
+          for (int i = 0; ok && i < n; ++i) {
+            const int bb = i & 1;
+            const bool more = i + 1 < n, end = i + 2 == n;
+            const uint32_t vu = bb ? a1 : a0, ku = bb ? a0 + 1 : a1;  // this V, the next K
+            if (!(ok = wait(kBarPFull, (st + i) & 1) && wait(kBarVFull + bb, vu & 1))) break;
             tc_fence_after();
-            qk(0, 0, false, n == 1);
-            qk(1, 0, true, n == 1);
-            for (int i = 0; ok && i < n; ++i) {
-              const int bb = i & 1;
-              const bool more = i + 1 < n, end = i + 2 == n;
-              const uint32_t vu = bb ? a1 : a0, ku = bb ? a0 + 1 : a1;  // this V, the next K
-              if (!(ok = wait(kBarPFull, (st + i) & 1) && wait(kBarVFull + bb, vu & 1))) break;
-              tc_fence_after();
-              pv(0, bb, i > 0, false);
-              if (more) {
-                if (!(ok = wait(kBarKFull + (bb ^ 1), ku & 1))) break;
-                qk(0, bb ^ 1, false, end);
-              }
-              if (!(ok = wait(kBarPFull + 1, (st + i) & 1))) break;
-              tc_fence_after();
-              pv(1, bb, i > 0, true);
-              if (more) qk(1, bb ^ 1, true, end);
-              if (bb) {
-                ++a0;
-                ++a1;
-              }
+            pv(0, bb, i > 0, false);
+            if (more) {
+              if (!(ok = wait(kBarKFull + (bb ^ 1), ku & 1))) break;
+              qk(0, bb ^ 1, false, end);
+            }
+            if (!(ok = wait(kBarPFull + 1, (st + i) & 1))) break;
+            tc_fence_after();
+            pv(1, bb, i > 0, true);
+            if (more) qk(1, bb ^ 1, true, end);
+            if (bb) {
+              ++a0;
+              ++a1;
             }
           }
-          u0 += (n + 1) / 2;
-          u1 += n / 2;
-          st += n;
-          ++segs;
         }
+        u0 += (n + 1) / 2;
+        u1 += n / 2;
+        st += n;
+        ++segs;
       }
-      // Then a stream each, whose products are a chain.  The second warp begins when the
-      // first has issued all of line 2 (no earlier: a barrier's phases are told apart by
-      // parity) and stream 1's last product of it, which is another thread's, is done.
-      __syncwarp();
-      asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (elect_one()) {  // the lane that was elected before
-        const int t = warp != kWarpMma;
-        uint32_t u = t ? u1 : u0;
-        if (t == 1 && st > 0) {
-          ok = wait(kBarODone + 1, (st - 1) & 1);
+    }
+    // Then a stream each, whose products are a chain.  The second warp begins when the
+    // first has issued all of line 2 (no earlier: a barrier's phases are told apart by
+    // parity) and stream 1's last product of it, which is another thread's, is done.
+    __syncwarp();
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    if (elect_one()) {  // the lane that was elected before
+      const int t = warp != kWarpMma;
+      uint32_t u = t ? u1 : u0;
+      if (t == 1 && st > 0) {
+        ok = wait(kBarODone + 1, (st - 1) & 1);
+        tc_fence_after();
+      }
+      begin(1 + t);
+      while (ok && next()) {
+        ok = wait(kBarQ + t, segs++ & 1);
+        for (int i = 0; ok && i < wk.s.nblk; ++i, ++u, ++st) {
+          if (!(ok = wait(kBarKFull + t, u & 1))) break;
           tc_fence_after();
-        }
-        begin(1 + t);
-        while (ok && next()) {
-          ok = wait(kBarQ + t, segs++ & 1);
-          for (int i = 0; ok && i < wk.s.nblk; ++i, ++u, ++st) {
-            if (!(ok = wait(kBarKFull + t, u & 1))) break;
-            tc_fence_after();
-            qk(t, t, true, i + 1 == wk.s.nblk);
-            if (!(ok = wait(kBarPFull + t, st & 1) && wait(kBarVFull + t, u & 1))) break;
-            tc_fence_after();
-            pv(t, t, i > 0, true);
-          }
+          qk(t, t, true, i + 1 == wk.s.nblk);
+          if (!(ok = wait(kBarPFull + t, st & 1) && wait(kBarVFull + t, u & 1))) break;
+          tc_fence_after();
+          pv(t, t, i > 0, true);
         }
       }
+    }
   } else {
     // ------------------------------------------------------------ softmax
     // A row is two threads', of warps four apart: half 0 has tokens 0 to 63 of each
@@ -485,237 +485,241 @@ __global__ void __launch_bounds__(kThreads, 1)
     int done = 0;            // blocks of the stream so far
     int u0 = 0, u1 = 0;      // uses of V's buffers so far
     for (int ln = 0; ln < 2; ++ln) {  // line 2, then the stream's share of line 1
-    begin(ln == 0 ? 0 : 1 + t);
-    // what the share leaves for the merge, if anything, is its last part
-    const bool tells = tt == 0 && half == 0 && (ln == 1 || t == 0);
-    if (tells) p.meta[2 * (ln == 0 ? wk.share : grid + wk.share)] = make_int4(0, 0, 0, 0);
-    while (next()) {
-      const int nt = wk.s.nblk;
-      int tok0 = wk.s.j0 * kTok;
-      const int row = wk.s.row0 + (two ? t * kRows : 0) + tt;  // node x g + head
-      const bool real = row < wk.n * G;
-      const bool busy = row - lane < wk.n * G;  // a warp without rows only keeps the barriers
-      const int past = wk.ctx - wk.n;
-      uint64_t mask = 0, any = 0;  // the nodes that the row sees, and that any row does
-      float m_ref = -INFINITY, l_sum = 0.f;
-      // The first part begins with a step on whatever lies in columns that no product
-      // uses yet, and drops what comes out: it brings the instructions into the cache
-      // while the first blocks are on their way (about 5000 cycles else).
-      int i = cold ? -1 : 0;
-      cold = false;
-      if (i < 0) tok0 -= kTok;
-      for (; i < nt; ++i, tok0 += kTok) {
-        const int kb = two ? i & 1 : t;  // the block's buffers, and their uses before
-        const int ku = (kb ? u1 : u0) + (two ? i >> 1 : i);
-        const uint32_t t_s = i < 0 ? t_free : t_sc;
-        if (i >= 0 && tok0 + kTok > past && (i == 0 || tok0 <= past)) {
-          // the first block with nodes: their words come while the scores are on their
-          // way (at the part's start they waited behind the last part's stores, 3000
-          // cycles: ragged trees 90.5 us, then 88)
-          const uint64_t nodes = wk.n == 64 ? ~0ull : (1ull << wk.n) - 1;
-          if (real) mask = (uint64_t)p.tree_mask[wk.q0 + row / G] & nodes;
-          any = lane < wk.n ? (uint64_t)p.tree_mask[wk.q0 + lane] : 0ull;
-          if (lane + 32 < wk.n) any |= (uint64_t)p.tree_mask[wk.q0 + lane + 32];
-          any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
-                 __reduce_or_sync(0xffffffffu, (uint32_t)any)) & nodes;
-        }
-        if (i >= 0) {
-          ok = ok && __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
-          tc_fence_after();
-        }
-        // a page outside the pool (reported by the copy warp, zeros in shared memory)
-        // is left out: bit pg stands for the block's page pg
-        const uint32_t bad = i < 0 ? 0 : bad_pages[2 * kb + (ku & 1)];
-        if (busy) {
-          uint32_t sa[16], sb[16];
-          if (i >= 0 && (tok0 + kTok > past || bad != 0)) {  // scores that the row does not see
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {  // a page
-              const int pg = 4 * half + k;
-              // bit e: whether the row sees token tok0 + 16 pg + e
-              const int s = tok0 + kPageSize * pg - past;  // of node 0, negative in the past
-              uint32_t v = s <= -16 ? 0xffffu : s >= 64 ? 0u : s >= 0 ? (uint32_t)(mask >> s)
-                           : (uint32_t)(mask << -s) | ((1u << -s) - 1);
-              if ((bad >> pg) & 1) v = 0;
-              if (__all_sync(0xffffffffu, (v & 0xffffu) == 0xffffu)) continue;
-              tmem_ld16_issue(t_s + 16 * k, sa);
-              tmem_ld16_wait(sa);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (!((v >> e) & 1)) sa[e] = 0xff800000u;  // -inf
-              tmem_st16_issue(t_s + 16 * k, sa);
-              tmem_st_wait();
-            }
+      begin(ln == 0 ? 0 : 1 + t);
+      // what the share leaves for the merge, if anything, is its last part
+      const bool tells = tt == 0 && half == 0 && (ln == 1 || t == 0);
+      if (tells) p.meta[2 * (ln == 0 ? wk.share : grid + wk.share)] = make_int4(0, 0, 0, 0);
+      while (next()) {
+        const int nt = wk.s.nblk;
+        int tok0 = wk.s.j0 * kTok;
+        const int row = wk.s.row0 + (two ? t * kRows : 0) + tt;  // node x g + head
+        const bool real = row < wk.n * G;
+        const bool busy = row - lane < wk.n * G;  // a warp without rows only keeps the barriers
+        const int past = wk.ctx - wk.n;
+        uint64_t mask = 0, any = 0;  // the nodes that the row sees, and that any row does
+        float m_ref = -INFINITY, l_sum = 0.f;
+        // The first part begins with a step on whatever lies in columns that no product
+        // uses yet, and drops what comes out: it brings the instructions into the cache
+        // while the first blocks are on their way (about 5000 cycles else).
+        int i = cold ? -1 : 0;
+        cold = false;
+        if (i < 0) tok0 -= kTok;
+        for (; i < nt; ++i, tok0 += kTok) {
+          const int kb = two ? i & 1 : t;  // the block's buffers, and their uses before
+          const int ku = (kb ? u1 : u0) + (two ? i >> 1 : i);
+          const uint32_t t_s = i < 0 ? t_free : t_sc;
+          if (i >= 0 && tok0 + kTok > past && (i == 0 || tok0 <= past)) {
+            // the first block with nodes: their words come while the scores are on their
+            // way (at the part's start they waited behind the last part's stores, 3000
+            // cycles: ragged trees 90.5 us, then 88)
+            const uint64_t nodes = wk.n == 64 ? ~0ull : (1ull << wk.n) - 1;
+            if (real) mask = (uint64_t)p.tree_mask[wk.q0 + row / G] & nodes;
+            any = lane < wk.n ? (uint64_t)p.tree_mask[wk.q0 + lane] : 0ull;
+            if (lane + 32 < wk.n) any |= (uint64_t)p.tree_mask[wk.q0 + lane + 32];
+            any = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
+                   __reduce_or_sync(0xffffffffu, (uint32_t)any)) & nodes;
           }
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto smax = [&](const uint32_t (&s)[16]) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              m4[e & 3] = max3(m4[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-          };
-          // 16 tokens at a time, from the last: the first are still in sa when P's turn
-          // comes
-          tmem_ld16_issue(t_s + 48, sb);
-          tmem_ld16_wait(sb);
-          tmem_ld16_issue(t_s + 32, sa);
-          smax(sb);
-          tmem_ld16_wait(sa);
-          tmem_ld16_issue(t_s + 16, sb);
-          smax(sa);
-          tmem_ld16_wait(sb);
-          tmem_ld16_issue(t_s, sa);
-          smax(sb);
-          tmem_ld16_wait(sa);
-          smax(sa);
-          float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), its;
-          ok = exchange(mx, ok, its);
-          mx = fmaxf(mx, its) * c2 - kRefBelow<BF16>;
-          const bool grow = mx > m_ref + 8.f;  // lazy rescale, as in the prefill kernel
-          float alpha = 1.f;
-          if (grow) {
-            alpha = ex2(m_ref - mx);
-            m_ref = mx;
-            l_sum *= alpha;
-          }
-          if (i > 0) {
-            ok = ok && __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + i - 1) & 1)));
+          if (i >= 0) {
+            ok = ok && __all_sync(0xffffffffu, wait(kBarSFull + t, (uint32_t)((done + i) & 1)));
             tc_fence_after();
-            if (ok && __any_sync(0xffffffffu, grow)) {
+          }
+          // a page outside the pool (reported by the copy warp, zeros in shared memory)
+          // is left out: bit pg stands for the block's page pg
+          const uint32_t bad = i < 0 ? 0 : bad_pages[2 * kb + (ku & 1)];
+          if (busy) {
+            uint32_t sa[16], sb[16];
+            if (i >= 0 && (tok0 + kTok > past || bad != 0)) {  // scores that the row does not see
 #pragma unroll 1
-              for (int cc = 0; cc < D / 64; ++cc) {
-                uint32_t r[32];
-                tmem_ld32(t_o + (uint32_t)cc * 32, r);
+              for (int k = 0; k < 4; ++k) {  // a page
+                const int pg = 4 * half + k;
+                // bit e: whether the row sees token tok0 + 16 pg + e
+                const int s = tok0 + kPageSize * pg - past;  // of node 0, negative in the past
+                uint32_t v = s <= -16 ? 0xffffu : s >= 64 ? 0u : s >= 0 ? (uint32_t)(mask >> s)
+                             : (uint32_t)(mask << -s) | ((1u << -s) - 1);
+                if ((bad >> pg) & 1) v = 0;
+                if (__all_sync(0xffffffffu, (v & 0xffffu) == 0xffffu)) continue;
+                tmem_ld16_issue(t_s + 16 * k, sa);
+                tmem_ld16_wait(sa);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                tmem_st32(t_o + (uint32_t)cc * 32, r);
+                for (int e = 0; e < 16; ++e)
+                  if (!((v >> e) & 1)) sa[e] = 0xff800000u;  // -inf
+                tmem_st16_issue(t_s + 16 * k, sa);
+                tmem_st_wait();
               }
             }
-          }
-          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t c2x2 = f2(c2, c2), nmu2 = f2(-mu, -mu);
-          uint64_t acc[2] = {0ull, 0ull};
-          // P of 16 tokens over their scores: eight columns of hi pairs, eight of lo pairs
-          auto weigh = [&](const uint32_t (&s)[16], uint32_t c) {
-            uint32_t pq[16];
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto smax = [&](const uint32_t (&s)[16]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 y = f2_split(fma2(f2(__uint_as_float(s[2 * e]),
-                                                __uint_as_float(s[2 * e + 1])), c2x2, nmu2));
-              const float p0 = ex2(y.x), p1 = ex2(y.y);
-              const uint64_t pp = f2(p0, p1);
-              acc[e & 1] = add2(acc[e & 1], pp);
-              pq[e] = pack2<BF16>(p0, p1);
-              const float2 hf = floats_of<BF16>(pq[e]);
-              const float2 l = f2_split(sub2(pp, f2(hf.x, hf.y)));
-              pq[8 + e] = pack2<BF16>(l.x, l.y);
+              for (int e = 0; e < 8; ++e)
+                m4[e & 3] =
+                    max3(m4[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+            };
+            // 16 tokens at a time, from the last: the first are still in sa when P's turn
+            // comes
+            tmem_ld16_issue(t_s + 48, sb);
+            tmem_ld16_wait(sb);
+            tmem_ld16_issue(t_s + 32, sa);
+            smax(sb);
+            tmem_ld16_wait(sa);
+            tmem_ld16_issue(t_s + 16, sb);
+            smax(sa);
+            tmem_ld16_wait(sb);
+            tmem_ld16_issue(t_s, sa);
+            smax(sb);
+            tmem_ld16_wait(sa);
+            smax(sa);
+            float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), its;
+            ok = exchange(mx, ok, its);
+            mx = fmaxf(mx, its) * c2 - kRefBelow<BF16>;
+            const bool grow = mx > m_ref + 8.f;  // lazy rescale, as in the prefill kernel
+            float alpha = 1.f;
+            if (grow) {
+              alpha = ex2(m_ref - mx);
+              m_ref = mx;
+              l_sum *= alpha;
             }
-            tmem_st16_issue(t_s + c, pq);
-          };
-          tmem_ld16_issue(t_s + 16, sb);
-          weigh(sa, 0);
-          tmem_ld16_wait(sb);
-          tmem_ld16_issue(t_s + 32, sa);
-          weigh(sb, 16);
-          tmem_ld16_wait(sa);
-          tmem_ld16_issue(t_s + 48, sb);
-          weigh(sa, 32);
-          tmem_ld16_wait(sb);
-          weigh(sb, 48);
-          tmem_st_wait();
-          const float2 a0 = f2_split(add2(acc[0], acc[1]));
-          l_sum += a0.x + a0.y;
-        }
-        if (i < 0) {
-          m_ref = -INFINITY;
-          l_sum = 0.f;
-          continue;
-        }
-        // V rows behind the end, and of nodes that no row sees, may hold anything
-        // (0 x NaN): zeroed in the staged block by the stream that uses it first
-        if (tok0 + kTok > past && (t == 0 || !two)) {
-          ok = ok && __all_sync(0xffffffffu, wait(kBarVFull + kb, (uint32_t)(ku & 1)));
-          const int first = max(0, past - tok0);
-          const uint32_t vb = base + kOffV + (uint32_t)kb * NH * kHalf;
-          for (int e = half * kRows + tt; ok && e < (kTok - first) * 8 * NH; e += kSoft) {
-            const int rr = first + e / (8 * NH), ch = e % (8 * NH), node = tok0 + rr - past;
-            if (node < wk.n && ((any >> node) & 1)) continue;
-            const uint32_t a = vb + (uint32_t)(ch >> 3) * kHalf + (uint32_t)rr * 128 +
-                               (uint32_t)(ch & 7) * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
-          }
-          // the tensor cores read them through the async proxy
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar(kBarPFull + t));
-      }
-      // ---- the part's end: the row's output, or the part's m, l and unnormalised o
-      ok = ok && __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + nt - 1) & 1)));
-      done += nt;
-      u0 += two ? (nt + 1) / 2 : nt;
-      u1 += two ? nt / 2 : nt;
-      const bool head = wk.s.j0 > 0, ends = wk.s.j0 + nt == wk.s.total, whole = !head && ends;
-      if (tells && !whole && !head) {  // the shares that hold the rest follow this one
-        const int64_t cost = line[p.B];
-        const int parts = (int)tree_share_of(wk.at - kTreeBlock, cost,
-                                             tree_shares(cost, two ? grid : 2 * grid)) - wk.share + 1;
-        const int64_t o = (int64_t)(wk.q0 + wk.s.row0 / G) * p.Hq + wk.s.h * G;
-        // parts, rows; the output row of the first
-        int4* const meta = p.meta + 2 * (ln == 0 ? wk.share : grid + wk.share);
-        meta[0] = make_int4(parts, min(two ? 2 * kRows : kRows, wk.n * G - wk.s.row0), 0, 0);
-        meta[1] = make_int4((int)(o & 0xffffffff), (int)(o >> 32), 0, 0);
-      }
-      if (busy) {
-        float its;
-        ok = exchange(l_sum, ok, its);
-        l_sum = half == 0 ? l_sum + its : its + l_sum;  // the same sum in both
-      }
-      if (ok && busy) {
-        tc_fence_after();
-        const bool some = l_sum != 0.f;  // NaN counts: it has to show
-        const int64_t prow = (2 * (int64_t)wk.share + (head ? 0 : 1)) * (two ? 2 * kRows : kRows) +
-                             (two ? t * kRows : 4 * kRows * (int64_t)grid) + tt;
-        float* const po = p.part_o + part_at<D>(prow) + half * (D / 16) * kPartStep;
-        const float inv = some ? 1.f / l_sum : 0.f;
-        const int64_t orow = (int64_t)(wk.q0 + row / G) * p.Hq + wk.s.h * G + row % G;
-        if (!whole && real && half == 0)
-          p.part_ml[prow] = some ? make_float2(m_ref, l_sum) : make_float2(-INFINITY, 0.f);
+            if (i > 0) {
+              ok = ok &&
+                   __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + i - 1) & 1)));
+              tc_fence_after();
+              if (ok && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
-        for (int cc = 0; cc < D / 64; ++cc) {
-          uint32_t r[32];
-          tmem_ld32(t_o + (uint32_t)cc * 32, r);
-          if (!real) continue;
-          const int col = half * (D / 2) + cc * 32;
-          if (!whole) {
+                for (int cc = 0; cc < D / 64; ++cc) {
+                  uint32_t r[32];
+                  tmem_ld32(t_o + (uint32_t)cc * 32, r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store32(po + (4 * cc + e) * kPartStep, r + 8 * e);
+                  for (int e = 0; e < 32; ++e)
+                    r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                  tmem_st32(t_o + (uint32_t)cc * 32, r);
+                }
+              }
+            }
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+            const uint64_t c2x2 = f2(c2, c2), nmu2 = f2(-mu, -mu);
+            uint64_t acc[2] = {0ull, 0ull};
+            // P of 16 tokens over their scores: eight columns of hi pairs, eight of lo pairs
+            auto weigh = [&](const uint32_t (&s)[16], uint32_t c) {
+              uint32_t pq[16];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 y = f2_split(fma2(f2(__uint_as_float(s[2 * e]),
+                                                  __uint_as_float(s[2 * e + 1])), c2x2, nmu2));
+                const float p0 = ex2(y.x), p1 = ex2(y.y);
+                const uint64_t pp = f2(p0, p1);
+                acc[e & 1] = add2(acc[e & 1], pp);
+                pq[e] = pack2<BF16>(p0, p1);
+                const float2 hf = floats_of<BF16>(pq[e]);
+                const float2 l = f2_split(sub2(pp, f2(hf.x, hf.y)));
+                pq[8 + e] = pack2<BF16>(l.x, l.y);
+              }
+              tmem_st16_issue(t_s + c, pq);
+            };
+            tmem_ld16_issue(t_s + 16, sb);
+            weigh(sa, 0);
+            tmem_ld16_wait(sb);
+            tmem_ld16_issue(t_s + 32, sa);
+            weigh(sb, 16);
+            tmem_ld16_wait(sa);
+            tmem_ld16_issue(t_s + 48, sb);
+            weigh(sa, 32);
+            tmem_ld16_wait(sb);
+            weigh(sb, 48);
+            tmem_st_wait();
+            const float2 a0 = f2_split(add2(acc[0], acc[1]));
+            l_sum += a0.x + a0.y;
+          }
+          if (i < 0) {
+            m_ref = -INFINITY;
+            l_sum = 0.f;
             continue;
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
-          uint4* to;  // (the output need not be aligned to whole sectors)
-          if (p.out_dtype == PKV_F32) {
-            to = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + orow * D + col);
-#pragma unroll
-            for (int e = 4; e < 8; ++e)
-              to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-          } else {
-            to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D + col);
-            const bool bf = p.out_dtype == PKV_BF16;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = __uint_as_float(r[2 * e]), y = __uint_as_float(r[2 * e + 1]);
-              r[e] = bf ? pack2<true>(x, y) : pack2<false>(x, y);
+          // V rows behind the end, and of nodes that no row sees, may hold anything
+          // (0 x NaN): zeroed in the staged block by the stream that uses it first
+          if (tok0 + kTok > past && (t == 0 || !two)) {
+            ok = ok && __all_sync(0xffffffffu, wait(kBarVFull + kb, (uint32_t)(ku & 1)));
+            const int first = max(0, past - tok0);
+            const uint32_t vb = base + kOffV + (uint32_t)kb * NH * kHalf;
+            for (int e = half * kRows + tt; ok && e < (kTok - first) * 8 * NH; e += kSoft) {
+              const int rr = first + e / (8 * NH), ch = e % (8 * NH), node = tok0 + rr - past;
+              if (node < wk.n && ((any >> node) & 1)) continue;
+              const uint32_t a = vb + (uint32_t)(ch >> 3) * kHalf + (uint32_t)rr * 128 +
+                                 (uint32_t)(ch & 7) * 16;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
             }
+            // the tensor cores read them through the async proxy
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          tc_fence_before();
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(bar(kBarPFull + t));
         }
-        tc_fence_before();  // O_t is read before P_t of the next part is handed over
+        // ---- the part's end: the row's output, or the part's m, l and unnormalised o
+        ok = ok && __all_sync(0xffffffffu, wait(kBarODone + t, (uint32_t)((done + nt - 1) & 1)));
+        done += nt;
+        u0 += two ? (nt + 1) / 2 : nt;
+        u1 += two ? nt / 2 : nt;
+        const bool head = wk.s.j0 > 0, ends = wk.s.j0 + nt == wk.s.total, whole = !head && ends;
+        if (tells && !whole && !head) {  // the shares that hold the rest follow this one
+          const int64_t cost = line[p.B];
+          const int64_t shares = tree_shares(cost, two ? grid : 2 * grid);
+          const int parts = (int)tree_share_of(wk.at - kTreeBlock, cost, shares) - wk.share + 1;
+          const int64_t o = (int64_t)(wk.q0 + wk.s.row0 / G) * p.Hq + wk.s.h * G;
+          // parts, rows; the output row of the first
+          int4* const meta = p.meta + 2 * (ln == 0 ? wk.share : grid + wk.share);
+          meta[0] = make_int4(parts, min(two ? 2 * kRows : kRows, wk.n * G - wk.s.row0), 0, 0);
+          meta[1] = make_int4((int)(o & 0xffffffff), (int)(o >> 32), 0, 0);
+        }
+        if (busy) {
+          float its;
+          ok = exchange(l_sum, ok, its);
+          l_sum = half == 0 ? l_sum + its : its + l_sum;  // the same sum in both
+        }
+        if (ok && busy) {
+          tc_fence_after();
+          const bool some = l_sum != 0.f;  // NaN counts: it has to show
+          const int64_t prow =
+              (2 * (int64_t)wk.share + (head ? 0 : 1)) * (two ? 2 * kRows : kRows) +
+              (two ? t * kRows : 4 * kRows * (int64_t)grid) + tt;
+          float* const po = p.part_o + part_at<D>(prow) + half * (D / 16) * kPartStep;
+          const float inv = some ? 1.f / l_sum : 0.f;
+          const int64_t orow = (int64_t)(wk.q0 + row / G) * p.Hq + wk.s.h * G + row % G;
+          if (!whole && real && half == 0)
+            p.part_ml[prow] = some ? make_float2(m_ref, l_sum) : make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+          for (int cc = 0; cc < D / 64; ++cc) {
+            uint32_t r[32];
+            tmem_ld32(t_o + (uint32_t)cc * 32, r);
+            if (!real) continue;
+            const int col = half * (D / 2) + cc * 32;
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) store32(po + (4 * cc + e) * kPartStep, r + 8 * e);
+              continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+            uint4* to;  // (the output need not be aligned to whole sectors)
+            if (p.out_dtype == PKV_F32) {
+              to = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + orow * D + col);
+#pragma unroll
+              for (int e = 4; e < 8; ++e)
+                to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+            } else {
+              to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D + col);
+              const bool bf = p.out_dtype == PKV_BF16;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float x = __uint_as_float(r[2 * e]), y = __uint_as_float(r[2 * e + 1]);
+                r[e] = bf ? pack2<true>(x, y) : pack2<false>(x, y);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          }
+          tc_fence_before();  // O_t is read before P_t of the next part is handed over
+        }
       }
-    }
     }
   }
 
